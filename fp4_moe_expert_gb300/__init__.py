@@ -21,6 +21,7 @@ FME_BF16 = 1
 
 # Every symbol include/fme.h declares, with its ctypes signature.
 _c_int, _c_size, _vp, _c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+_c_ll = ctypes.c_longlong
 SIGNATURES = {
     "fme_last_error": (ctypes.c_char_p, []),
     "fme_version": (_c_int, []),
@@ -48,6 +49,18 @@ SIGNATURES = {
     "fme_combine_rmsnorm": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _c_float, _vp, _vp, _vp]),
     "fme_moe_layer_nvfp4": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                      _c_int, _c_int, _c_int, _c_float, _c_float, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "fme_add_rmsnorm_fp8": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _c_int, _c_int, _c_float, _c_int, _vp, _vp, _vp,
+                                     _vp, _vp]),
+    "fme_add_rmsnorm_mxfp8": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp,
+                                       _vp]),
+    "fme_moe_route": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _c_size, _vp]),
+    "fme_moe_route_workspace": (_c_size, [_c_int] * 3),
+    "fme_moe_grouped_swiglu_fp8": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                            _c_float, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "fme_moe_grouped_gemm_fp8": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                          _vp, _c_int, _vp, _c_size, _vp]),
+    "fme_moe_grouped_fp8_workspace": (_c_size, [_c_int] * 4),
     "fme_workspace_clear": (_c_int, [_vp, _c_size, _vp]),
     "fme_selftest_wait_timeout": (_c_int, [_vp, _c_size, _c_int, _vp]),
     "fme_workspace_error": (_c_int, [_vp, ctypes.POINTER(_c_int), _vp]),
@@ -343,6 +356,182 @@ def ue8m0_unpack(packed, n, k, check=True):
     if check and int(flag[0].item()) != 0:
         raise ValueError("scales vary inside a 128-row block")
     return dst
+
+
+def _stream_workspace(nbytes, device, workspace):
+    """The caller's workspace, or one kept per device, current stream and size."""
+    if workspace is not None:
+        return _workspace(nbytes, device, workspace)
+    key = (device, torch.cuda.current_stream(device).cuda_stream, nbytes)
+    ws = _ws_cache.get(key)
+    if ws is None:
+        ws = _ws_cache[key] = Workspace(nbytes, device)
+    return ws
+
+
+def _rows(t, name):
+    """A BF16 CUDA matrix with dense rows, any row stride that is a multiple of 8."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a CUDA bfloat16 matrix with contiguous rows, got {t.dtype} "
+                         f"{tuple(t.shape)} strides={t.stride()} cuda={t.is_cuda}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8)
+
+
+def _out(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, shape, name)
+    return t
+
+
+def _add_rmsnorm(x, gamma, residual, eps, mx, ue8m0, want_normed, q, scales, normed, residual_out):
+    ldx, dev = _rows(x, "x"), x.device
+    T, H = x.shape
+    _need(gamma, torch.bfloat16, (H,), "gamma")
+    ldr = H
+    if residual is not None:
+        ldr = _rows(residual, "residual")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual: expected {tuple(x.shape)}, got {tuple(residual.shape)}")
+        residual_out = _out(residual_out, (T, H), torch.bfloat16, dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    q = _out(q, (T, H), torch.uint8, dev, "q")
+    if mx:
+        scales = _out(scales, (T, H // 32), torch.uint8, dev, "scales")
+    else:
+        scales = _out(scales, (T, H // 128), torch.float32, dev, "scales")
+    if want_normed or normed is not None:
+        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+    if T == 0:
+        return q, scales, residual_out, normed
+    args = (_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), T, H, float(eps))
+    outs = (_ptr(q), _ptr(scales), _ptr(normed), _ptr(residual_out), _stream(dev))
+    if mx:
+        _check(lib.fme_add_rmsnorm_mxfp8(*args, *outs))
+    else:
+        _check(lib.fme_add_rmsnorm_fp8(*args, int(bool(ue8m0)), *outs))
+    return q, scales, residual_out, normed
+
+
+def add_rmsnorm_fp8(x, gamma, residual=None, eps=1e-5, ue8m0=False, want_normed=False, q=None, scales=None,
+                    normed=None, residual_out=None):
+    """Residual addition, RMSNorm and FP8 quantisation (fme_add_rmsnorm_fp8) of x [T, H] BF16 (any row stride) with
+    gamma [H] BF16. Returns (q [T, H] uint8 E4M3, scales [T, H/128] float32, residual_out [T, H] BF16 or None without
+    a residual, normed [T, H] BF16 or None unless wanted). residual_out may be residual itself."""
+    return _add_rmsnorm(x, gamma, residual, eps, False, ue8m0, want_normed, q, scales, normed, residual_out)
+
+
+def add_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, want_normed=False, q=None, scales=None, normed=None,
+                      residual_out=None):
+    """add_rmsnorm_fp8 in the MXFP8 format (fme_add_rmsnorm_mxfp8): scales [T, H/32] uint8 E8M0, as
+    moe_routed_fp8_mx takes them."""
+    return _add_rmsnorm(x, gamma, residual, eps, True, False, want_normed, q, scales, normed, residual_out)
+
+
+def moe_route_workspace(T, E, top_k):
+    return lib.fme_moe_route_workspace(T, E, top_k)
+
+
+def moe_route(logits, bias, top_k, scale=1.0, ids=None, weights=None, offsets=None, rows=None, tokens=None,
+              workspace=None):
+    """Routing of T tokens and their routes grouped by expert (fme_moe_route): logits [T, E] bf16 or float32, bias [E]
+    float32. Returns ids [T, top_k] int32, weights [T, top_k] float32, offsets [E + 1] int32 (expert e holds places
+    offsets[e] .. offsets[e + 1] - 1), rows [T * top_k] int32 (the route t * top_k + r at each place) and tokens
+    [T * top_k] int32 (its token)."""
+    T, E = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be float32 or bfloat16")
+    _need(logits, logits.dtype, (T, E), "logits")
+    _need(bias, torch.float32, (E,), "bias")
+    ids = _out(ids, (T, top_k), torch.int32, dev, "ids")
+    weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
+    offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets")
+    rows = _out(rows, (T * top_k,), torch.int32, dev, "rows")
+    tokens = _out(tokens, (T * top_k,), torch.int32, dev, "tokens")
+    if T == 0:
+        return ids, weights, offsets.zero_(), rows, tokens
+    ws = _stream_workspace(moe_route_workspace(T, E, top_k), dev, workspace)
+    ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
+    _check(lib.fme_moe_route(_ptr(logits), ldt, _ptr(bias), T, E, top_k, float(scale), _ptr(ids), _ptr(weights),
+                             _ptr(offsets), _ptr(rows), _ptr(tokens), ws.ptr(), ws.nbytes, _stream(dev)))
+    return ids, weights, offsets, rows, tokens
+
+
+def moe_grouped_fp8_workspace(R, K, N, E):
+    return lib.fme_moe_grouped_fp8_workspace(R, K, N, E)
+
+
+def _need_grouped(a, sa, w, sw, offsets, in_rows):
+    """Checks the operands the grouped products share; returns (a_rows, K, E, N, R)."""
+    E, N, K = w.shape
+    a_rows = a.shape[0]
+    _need(a, torch.uint8, (a_rows, K), "a")
+    _need(sa, torch.float32, (a_rows, K // 128), "sa")
+    _need(w, torch.uint8, (E, N, K), "w")
+    _need(sw, torch.float32, (E, N // 128, K // 128), "sw")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    R = a_rows
+    if in_rows is not None:
+        R = in_rows.numel()
+        _need(in_rows, torch.int32, (R,), "in_rows")
+    return a_rows, K, E, N, R
+
+
+def moe_grouped_swiglu_fp8(a, sa, w13, s13, offsets, in_rows=None, limit=float("inf"), ue8m0=False, gate_first=False,
+                           q=None, scales=None, workspace=None):
+    """Gate/up product, SwiGLU and FP8 re-quantisation of rows grouped by expert (fme_moe_grouped_swiglu_fp8).
+
+    a [a_rows, H] uint8 E4M3 and sa [a_rows, H/128] float32; w13 [E, 2I, H] uint8 (up rows then gate rows, or the
+    other way with gate_first) and s13 [E, 2I/128, H/128] float32; offsets [E + 1] int32; in_rows [R] int32 (the row
+    of a at each place; None: the place itself). Returns q [R, I] uint8 E4M3 and scales [R, I/128] float32, at the
+    places; places no group holds are left as they are."""
+    a_rows, H, E, two_i, R = _need_grouped(a, sa, w13, s13, offsets, in_rows)
+    I = two_i // 2
+    dev = a.device
+    q = _out(q, (R, I), torch.uint8, dev, "q")
+    scales = _out(scales, (R, I // 128), torch.float32, dev, "scales")
+    if R == 0:
+        return q, scales
+    ws = _stream_workspace(moe_grouped_fp8_workspace(R, H, two_i, E), dev, workspace)
+    _check(lib.fme_moe_grouped_swiglu_fp8(_ptr(a), _ptr(sa), a_rows, _ptr(w13), _ptr(s13), _ptr(offsets),
+                                          _ptr(in_rows), R, H, I, E, float(limit), int(bool(ue8m0)),
+                                          int(bool(gate_first)), _ptr(q), _ptr(scales), ws.ptr(), ws.nbytes,
+                                          _stream(dev)))
+    return q, scales
+
+
+def moe_grouped_gemm_fp8(a, sa, w, sw, offsets, in_rows=None, out_rows=None, out=None, workspace=None):
+    """Product of rows grouped by expert, BF16 out (fme_moe_grouped_gemm_fp8): a [a_rows, K], w [E, N, K] and their
+    scales as moe_grouped_swiglu_fp8; out_rows [R] int32 (the output row of each place; None: the place itself).
+    Returns out [R, N] BF16 (or the given out [out_n, N]); rows no place names are left as they are."""
+    a_rows, K, E, N, R = _need_grouped(a, sa, w, sw, offsets, in_rows)
+    dev = a.device
+    if out_rows is not None:
+        _need(out_rows, torch.int32, (R,), "out_rows")
+    if out is None:
+        out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, (out.shape[0], N), "out")
+    if R == 0:
+        return out
+    ws = _stream_workspace(moe_grouped_fp8_workspace(R, K, N, E), dev, workspace)
+    _check(lib.fme_moe_grouped_gemm_fp8(_ptr(a), _ptr(sa), a_rows, _ptr(w), _ptr(sw), _ptr(offsets), _ptr(in_rows),
+                                        _ptr(out_rows), R, K, N, E, _ptr(out), out.shape[0], ws.ptr(), ws.nbytes,
+                                        _stream(dev)))
+    return out
+
+
+def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, shared_out=None):
+    """The routed FP8 experts of a prompt of T tokens, combined: moe_route, moe_grouped_swiglu_fp8 on the tokens' rows,
+    moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
+
+    xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
+    weights these are. Returns (y [T, H] BF16, ids, weights)."""
+    ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale)
+    hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0)
+    out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows)
+    return moe_finalize(out, weights, shared_out), ids, weights
 
 
 def moe_routed_nvfp4_workspace(M, H, N, L, top_k):

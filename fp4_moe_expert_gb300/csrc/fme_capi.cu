@@ -415,6 +415,157 @@ int fme_moe_routed_nvfp4(const void* x, const int32_t* topk_ids, const float* to
                       workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
+static int check_norm(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T, int H,
+                      int block, float eps, const void* q, const void* scales, const void* normed,
+                      const void* residual_out) {
+  FME_REQUIRE(x && gamma && q && scales && (residual == nullptr) == (residual_out == nullptr), FME_EINVAL,
+              "null pointer argument (residual and residual_out come together)");
+  FME_REQUIRE(T >= 0 && T <= (1 << 20), FME_EINVAL, "T=%d outside [0, 2^20]", T);
+  FME_REQUIRE(H >= block && H % block == 0 && H <= 16384, FME_EINVAL, "H=%d must be a multiple of %d in [%d, 16384]", H,
+              block, block);
+  FME_REQUIRE(ldx >= H && ldx % 8 == 0 && (residual == nullptr || (ldr >= H && ldr % 8 == 0)), FME_EINVAL,
+              "row strides ldx=%lld, ldr=%lld must be multiples of 8 and at least H=%d", ldx, ldr, H);
+  FME_REQUIRE(residual_out != residual || residual == nullptr || ldr == H, FME_EINVAL,
+              "residual_out may be residual only when its rows are dense (ldr=%lld)", ldr);
+  FME_REQUIRE(eps >= 0.0f && std::isfinite(eps), FME_EINVAL, "eps must be finite and >= 0");
+  FME_REQUIRE(!misaligned(x) && !misaligned(residual) && !misaligned(gamma) && !misaligned(q) && !misaligned(normed) &&
+                  !misaligned(residual_out),
+              FME_EALIGN, "every pointer must be 16-byte aligned");
+  return FME_OK;
+}
+
+int fme_add_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T,
+                        int H, float eps, int ue8m0, uint8_t* q, float* scales, void* normed, void* residual_out,
+                        void* stream) {
+  const int st = check_norm(x, ldx, residual, ldr, gamma, T, H, 128, eps, q, scales, normed, residual_out);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(!misaligned(scales), FME_EALIGN, "scales must be 16-byte aligned");
+  if (T == 0) return FME_OK;
+  return add_rmsnorm_quant(x, ldx, residual, ldr, gamma, T, H, eps, ue8m0, q, scales, nullptr, normed, residual_out,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T,
+                          int H, float eps, uint8_t* q, uint8_t* scales, void* normed, void* residual_out,
+                          void* stream) {
+  const int st = check_norm(x, ldx, residual, ldr, gamma, T, H, 32, eps, q, scales, normed, residual_out);
+  if (st != FME_OK) return st;
+  if (T == 0) return FME_OK;
+  return add_rmsnorm_quant(x, ldx, residual, ldr, gamma, T, H, eps, 0, q, nullptr, scales, normed, residual_out,
+                           static_cast<cudaStream_t>(stream));
+}
+
+static int check_route_shapes(int T, int E, int top_k) {
+  FME_REQUIRE(T >= 0 && T <= (1 << 20), FME_EINVAL, "T=%d outside [0, 2^20]", T);
+  FME_REQUIRE(E >= 1 && E <= kMaxExperts, FME_EUNSUPPORTED, "E=%d outside [1, %d]", E, kMaxExperts);
+  FME_REQUIRE(top_k >= 1 && top_k <= E && top_k <= kMaxTopK, FME_EINVAL, "top_k=%d outside [1, min(E=%d, %d)]", top_k,
+              E, kMaxTopK);
+  return FME_OK;
+}
+
+size_t fme_moe_route_workspace(int T, int E, int top_k) {
+  if (check_route_shapes(T, E, top_k) != FME_OK) return 0;
+  return route_workspace_bytes(T, E);
+}
+
+int fme_moe_route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale,
+                  int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  FME_REQUIRE(logits && bias && ids && weights && offsets && rows && tokens, FME_EINVAL, "null pointer argument");
+  const int st = check_route_shapes(T, E, top_k);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(logits_dtype == FME_F32 || logits_dtype == FME_BF16, FME_EINVAL, "logits_dtype=%d", logits_dtype);
+  FME_REQUIRE(std::isfinite(scale), FME_EINVAL, "scale must be finite");
+  FME_REQUIRE(!misaligned(logits) && !misaligned(bias) && !misaligned(ids) && !misaligned(weights) &&
+                  !misaligned(offsets) && !misaligned(rows) && !misaligned(tokens) && !misaligned(workspace),
+              FME_EALIGN, "every pointer must be 16-byte aligned");
+  return route(logits, logits_dtype, bias, T, E, top_k, scale, ids, weights, offsets, rows, tokens, workspace,
+               workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+static int check_grouped_shapes(int R, int K, int N, int E) {
+  FME_REQUIRE(R >= 0 && R <= (1 << 25), FME_EINVAL, "R=%d outside [0, 2^25]", R);
+  FME_REQUIRE(K >= 128 && K % 128 == 0 && N >= 128 && N % 128 == 0, FME_EINVAL,
+              "%d values and %d weight rows must be positive multiples of 128", K, N);
+  FME_REQUIRE(K <= 16384 && N <= 16384, FME_EUNSUPPORTED, "%d values or %d weight rows above 16384", K, N);
+  FME_REQUIRE(E >= 1 && E <= kMaxExperts, FME_EUNSUPPORTED, "E=%d outside [1, %d]", E, kMaxExperts);
+  return FME_OK;
+}
+
+size_t fme_moe_grouped_fp8_workspace(int R, int K, int N, int E) {
+  if (check_grouped_shapes(R, K, N, E) != FME_OK) return 0;
+  return grouped_fp8_workspace_bytes();
+}
+
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+int fme_moe_grouped_swiglu_fp8(const uint8_t* a, const float* sa, int a_rows, const uint8_t* w13, const float* s13,
+                               const int32_t* offsets, const int32_t* in_rows, int R, int H, int I, int E, float limit,
+                               int ue8m0, int gate_first, uint8_t* q, float* scales, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  FME_REQUIRE(a && sa && w13 && s13 && offsets && q && scales, FME_EINVAL, "null pointer argument");
+  FME_REQUIRE(I >= 128 && I <= 8192, FME_EINVAL, "I=%d outside [128, 8192]", I);
+  const int st = check_grouped_shapes(R, H, 2 * I, E);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(I % 128 == 0, FME_EINVAL, "I=%d must be a multiple of 128", I);
+  FME_REQUIRE(a_rows >= 1 && a_rows <= (1 << 25) && (in_rows != nullptr || a_rows >= R), FME_EINVAL,
+              "a_rows=%d outside [1, 2^25], or below R=%d without in_rows", a_rows, R);
+  FME_REQUIRE(limit > 0.0f, FME_EINVAL, "limit must be > 0 (got %g)", static_cast<double>(limit));
+  FME_REQUIRE(!misaligned(a) && !misaligned(sa) && !misaligned(w13) && !misaligned(s13) && !misaligned(q) &&
+                  !misaligned(scales) && !misaligned(workspace) && !misaligned4(offsets) && !misaligned4(in_rows),
+              FME_EALIGN, "every pointer must be 16-byte aligned (offsets and in_rows: 4-byte)");
+  GroupedFp8 g;
+  g.a = a;
+  g.sa = sa;
+  g.a_rows = a_rows;
+  g.w = w13;
+  g.sw = s13;
+  g.offsets = offsets;
+  g.in_rows = in_rows;
+  g.R = R;
+  g.K = H;
+  g.N = 2 * I;
+  g.E = E;
+  g.limit = limit;
+  g.ue8m0 = ue8m0;
+  g.gate_first = gate_first;
+  g.q = q;
+  g.sq = scales;
+  return grouped_fp8(g, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int fme_moe_grouped_gemm_fp8(const uint8_t* a, const float* sa, int a_rows, const uint8_t* w, const float* sw,
+                             const int32_t* offsets, const int32_t* in_rows, const int32_t* out_rows, int R, int K,
+                             int N, int E, void* out, int out_n, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  FME_REQUIRE(a && sa && w && sw && offsets && out, FME_EINVAL, "null pointer argument");
+  const int st = check_grouped_shapes(R, K, N, E);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(a_rows >= 1 && a_rows <= (1 << 25) && (in_rows != nullptr || a_rows >= R), FME_EINVAL,
+              "a_rows=%d outside [1, 2^25], or below R=%d without in_rows", a_rows, R);
+  FME_REQUIRE(out_n >= 1 && out_n <= (1 << 25) && (out_rows != nullptr || out_n >= R), FME_EINVAL,
+              "out_n=%d outside [1, 2^25], or below R=%d without out_rows", out_n, R);
+  FME_REQUIRE(!misaligned(a) && !misaligned(sa) && !misaligned(w) && !misaligned(sw) && !misaligned(out) &&
+                  !misaligned(workspace) && !misaligned4(offsets) && !misaligned4(in_rows) && !misaligned4(out_rows),
+              FME_EALIGN, "every pointer must be 16-byte aligned (offsets, in_rows and out_rows: 4-byte)");
+  GroupedFp8 g;
+  g.a = a;
+  g.sa = sa;
+  g.a_rows = a_rows;
+  g.w = w;
+  g.sw = sw;
+  g.offsets = offsets;
+  g.in_rows = in_rows;
+  g.out_rows = out_rows;
+  g.R = R;
+  g.out_n = out_n;
+  g.K = K;
+  g.N = N;
+  g.E = E;
+  g.out = out;
+  return grouped_fp8(g, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
 int fme_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int timeout_ms, void* stream) {
   FME_REQUIRE(workspace != nullptr && workspace_bytes >= 512, FME_EWORKSPACE, "workspace of 512 bytes needed");
   FME_REQUIRE(timeout_ms > 0 && timeout_ms <= 10000, FME_EINVAL, "timeout_ms=%d outside [1, 10000]", timeout_ms);

@@ -1,0 +1,448 @@
+// Matrix products grouped by expert, E4M3 x E4M3 with FP32 block scales, for
+// any number of tokens: the prompt-side counterpart of the routed decode
+// kernel, on the same resident weights.
+//
+// Group e holds rows p in [offsets[e], offsets[e + 1]). Per row and weight row n
+//   y[p, n] = sum_b (sum_{k in block b} W[e, n, k] a[r, k]) * (sw[e, n/128, b] * sa[r, b]),
+// r = in_rows[p]. Two epilogues:
+//   gemm    out[out_rows[p], n] = bf16(y[p, n]);
+//   swiglu  h = silu(min(gate, limit)) * clamp(up, -limit, limit),
+//           s = max(amax over 128 hidden values, 1e-10) / 448, q = e4m3(h / s).
+//
+// One persistent CTA per SM walks tiles of 128 rows of a group x 256 weight rows
+// (swiglu: the 128 up rows and the 128 gate rows of one 128-value hidden
+// block, so its quantisation block is inside the tile and one thread holds
+// both halves of a value). Ten warps: 0-7 accumulate, 8 loads, 9 issues the MMA.
+// * Loads: per 128-value K block two 128-row boxes of weights and the tile's rows
+//   gathered by TMA (tile::gather4, four rows a lane), only the rows the group
+//   has: a group of one row moves 512 bytes of activations beside its 32 KB of
+//   weights.
+// * The scales are FP32 and not powers of two, so the MMA cannot apply them: each
+//   K block is one 128 x 256 accumulation in tensor memory (two buffers), and the
+//   accumulate warps add D * (sw * sa) into 128 registers a thread. A row is a
+//   tensor-memory lane, so sa is one scalar a thread and sw one or two a tile.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "fme_common.cuh"
+#include "fme_internal.h"
+
+namespace fme {
+
+constexpr int kGrThreads = 320;
+constexpr int kGrAccWarps = 8;
+constexpr int kGrStages = 4;
+constexpr int kGrABytes = 128 * 128;
+constexpr int kGrBBytes = 256 * 128;
+constexpr int kGrStageBytes = kGrABytes + kGrBBytes;
+
+struct GrArgs {
+  CUtensorMap mapg;  // a as [a_rows, K bytes], box 1 row x 128 bytes (gather)
+  CUtensorMap mapw;  // weights as [E * N, K bytes], box 128 rows x 128 bytes
+  const float* sa;
+  const float* sw;
+  const int32_t* offsets;
+  const int32_t* in_rows;   // null: row p
+  const int32_t* out_rows;  // null: row p
+  int a_rows, R, out_n, K, N, E;
+  int up0, gate0;  // first up / gate weight row (swiglu)
+  float limit;
+  int ue8m0;
+  uint8_t* q;
+  float* sq;
+  __nv_bfloat16* out;
+  uint32_t* err;
+  unsigned long long timeout_ns;
+};
+
+struct GrShared {
+  uint64_t full[kGrStages], empty[kGrStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int warp_sum[kGrThreads / 32];
+  int off[kMaxExperts + 1];     // group starts, clamped to [0, R] and ascending
+  int tiles[kMaxExperts + 1];   // 128-row tiles before group e
+  float amax[2][2][128];        // [tile parity][column half][row]
+};
+
+constexpr size_t kGrSmemBytes = static_cast<size_t>(kGrStages) * kGrStageBytes + 1024 + sizeof(GrShared);
+static_assert(kGrSmemBytes <= 232448, "shared memory per CTA");
+
+struct GrTile {
+  int e, n, p0, rows;  // expert, weight tile, first row and row count
+};
+
+// Tile t: groups in order, within a group the row tiles of one weight tile are
+// neighbours, so CTAs running at the same time share the weights through L2.
+__device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles, int t) {
+  const int x = t / n_tiles;
+  int lo = 0, hi = E;  // tiles[lo] <= x < tiles[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (S.tiles[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int mt = S.tiles[lo + 1] - S.tiles[lo];
+  const int local = t - S.tiles[lo] * n_tiles;
+  GrTile g;
+  g.e = lo;
+  g.n = local / mt;
+  g.p0 = S.off[lo] + (local - g.n * mt) * 128;
+  g.rows = min(128, S.off[lo + 1] - g.p0);
+  return g;
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid_constant__ GrArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  GrShared& S = *reinterpret_cast<GrShared*>(ring + kGrStages * kGrStageBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int KB = a.K / 128;
+  const int n_tiles = SWIGLU ? a.N / 256 : (a.N + 255) / 256;
+
+  if (tid == 0) {
+    for (int s = 0; s < kGrStages; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&S.tfull[b], 1);
+      mbar_init(&S.tempty[b], kGrAccWarps);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&S.tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&a.mapg);
+    prefetch_tmap(&a.mapw);
+  }
+  griddep_wait();
+  // Row tiles before each group: every thread four groups, then a block scan.
+  constexpr int kPer = (kMaxExperts + kGrThreads - 1) / kGrThreads;
+  int own[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    own[i] = 0;
+    if (e < a.E) {
+      const int lo = max(0, min(a.R, __ldg(a.offsets + e)));
+      const int hi = max(lo, min(a.R, __ldg(a.offsets + e + 1)));
+      S.off[e] = lo;
+      own[i] = (hi - lo + 127) / 128;
+      if (e == a.E - 1) S.off[a.E] = hi;
+    }
+    sum += own[i];
+  }
+  int scan = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+    if (lane >= d) scan += v;
+  }
+  if (lane == 31) S.warp_sum[warp] = scan;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = scan - sum;
+  for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    if (e <= a.E) S.tiles[e] = before;
+    before += own[i];
+  }
+  __syncthreads();
+  const int total = S.tiles[a.E] * n_tiles;
+  const uint32_t tmem = S.tmem;
+  const volatile int* abort = &S.abort;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      int4 y;
+      int* yp = &y.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = g.p0 + min(4 * lane + i, g.rows - 1);
+        const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
+        yp[i] = r >= 0 && r < a.a_rows ? r : 0;  // a bad row is read as row 0 and written as zeros
+      }
+      const bool gather = 4 * lane < g.rows;
+      const int w0 = SWIGLU ? g.e * a.N + a.up0 + 128 * g.n : g.e * a.N + 256 * g.n;
+      const int w1 = SWIGLU ? g.e * a.N + a.gate0 + 128 * g.n : w0 + 128;
+      const bool two = SWIGLU || 256 * g.n + 128 < a.N;
+      const uint32_t bytes = 512u * ((g.rows + 3) / 4) + (two ? kGrBBytes : kGrBBytes / 2);
+      for (int j = 0; j < KB; ++j, ++it) {
+        const uint32_t s = it % kGrStages;
+        ok = mbar_wait(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        uint8_t* st = ring + s * kGrStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[s], bytes);
+        __syncwarp();
+        if (gather) tma_gather4(st + 512 * lane, &a.mapg, 128 * j, y, &S.full[s]);
+        if (lane == 0) tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, w0, &S.full[s]);
+        if (lane == 1 && two) tma_load_2d(st + kGrABytes + kGrBBytes / 2, &a.mapw, 128 * j, w1, &S.full[s]);
+      }
+    }
+    if (!ok) {
+      // Copies in flight must land before the CTA leaves its shared memory.
+      if (lane == 0) {
+        atomicOr(a.err, kErrRingWait);
+        S.abort = 1;
+        for (uint32_t k = it > kGrStages ? it - kGrStages : 0; k < it; ++k)
+          if (!mbar_wait(&S.full[k % kGrStages], (k / kGrStages) & 1, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int j = 0; j < KB; ++j, ++it) {
+          const uint32_t s = it % kGrStages, b = it & 1;
+          ok = mbar_wait(&S.tempty[b], ((it >> 1) & 1) ^ 1, a.timeout_ns, abort) &&
+               mbar_wait(&S.full[s], (it / kGrStages) & 1, a.timeout_ns, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring) + s * kGrStageBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tc_mma_f8(tmem + 256 * b, sw128_desc(st + 32 * i), sw128_desc(st + kGrABytes + 32 * i), f8_idesc(128, 256),
+                      i != 0);
+          tc_commit(&S.empty[s]);
+          tc_commit(&S.tfull[b]);
+        }
+      }
+      if (!ok) {
+        atomicOr(a.err, kErrRingWait);
+        S.abort = 1;
+        tc_commit(&S.drain);
+        if (!mbar_wait(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ accumulate and epilogue
+    const int half = warp >> 2, quad = warp & 3;
+    const int row = 32 * quad + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    const int wblocks = a.N / 128;  // 128-row weight blocks of one expert
+    uint32_t it = 0;
+    int parity = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, parity ^= 1) {
+      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      const bool columns = SWIGLU || 256 * g.n + 128 * half < a.N;
+      const bool live = 32 * quad < g.rows && columns;  // this warp has rows (and columns) to hold
+      const int p = g.p0 + min(row, g.rows - 1);
+      const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
+      const bool bad = r < 0 || r >= a.a_rows;
+      const float* sa = a.sa + static_cast<size_t>(bad ? 0 : r) * KB;
+      const int b0 = SWIGLU ? a.up0 / 128 + g.n : min(2 * g.n + half, wblocks - 1);
+      const int b1 = SWIGLU ? a.gate0 / 128 + g.n : b0;
+      const float* sw0 = a.sw + (static_cast<size_t>(g.e) * wblocks + b0) * KB;
+      const float* sw1 = a.sw + (static_cast<size_t>(g.e) * wblocks + b1) * KB;
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      for (int j = 0; j < KB; ++j, ++it) {
+        const uint32_t b = it & 1;
+        const float sx = __ldg(sa + j);
+        const float s0 = __fmul_rn(__ldg(sw0 + j), sx), s1 = SWIGLU ? __fmul_rn(__ldg(sw1 + j), sx) : s0;
+        ok = ok && mbar_wait(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (live) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float d[32];
+            const uint32_t col = SWIGLU ? (c >> 1) * 128 + 64 * half + 32 * (c & 1) : 128 * half + 32 * c;
+            tmem_ld_issue(lanes + 256 * b + col, d);
+            tmem_ld_join(d);
+            const float s = c < 2 ? s0 : s1;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(d[i], s, acc[32 * c + i]);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tempty[b]);
+      }
+      if (bad) {
+        if (row < g.rows && half == 0) atomicOr(a.err, kErrRoute);
+#pragma unroll
+        for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      }
+      if (SWIGLU) {
+        // acc[0..63] up, acc[64..127] gate of hidden values 64 * half .. + 63.
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const float up = fminf(fmaxf(acc[c], -a.limit), a.limit);
+          const float gate = fminf(acc[64 + c], a.limit);
+          acc[c] = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
+          amax = fmaxf(amax, fabsf(acc[c]));
+        }
+        S.amax[parity][half][row] = amax;
+        // Uniform over the eight warps, so none is left waiting at the next tile's barrier.
+        if (named_bar_or(1, 32 * kGrAccWarps, !ok)) {
+          ok = false;
+          break;
+        }
+        if (row < g.rows) {
+          amax = fmaxf(amax, S.amax[parity][half ^ 1][row]);
+          float s = __fdiv_rn(fmaxf(amax, 1e-10f), 448.0f);
+          if (a.ue8m0) s = ue8m0_ceil(s);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = f32x2_to_e4m3x2(__fdiv_rn(acc[4 * i], s), __fdiv_rn(acc[4 * i + 1], s)) |
+                   (f32x2_to_e4m3x2(__fdiv_rn(acc[4 * i + 2], s), __fdiv_rn(acc[4 * i + 3], s)) << 16);
+          const int I = a.N / 2;
+          uint4* dst = reinterpret_cast<uint4*>(a.q + static_cast<size_t>(p) * I + 128 * g.n + 64 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          if (half == 0) a.sq[static_cast<size_t>(p) * (I / 128) + g.n] = s;
+        }
+      } else {
+        if (!ok) break;
+        if (row < g.rows && columns) {
+          const int o = a.out_rows != nullptr ? __ldg(a.out_rows + p) : p;
+          if (o < 0 || o >= a.out_n) {
+            atomicOr(a.err, kErrRoute);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(o) * a.N + 256 * g.n + 128 * half);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(acc[8 * i + 2 * k]));
+                const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(acc[8 * i + 2 * k + 1]));
+                w[k] = lo | (hi << 16);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.err, kErrRingWait);
+      S.abort = 1;
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host side
+static PFN_cuTensorMapEncodeTiled_v12000 gr_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// Byte tensor [rows, cols], box box_rows x 128 bytes, 128-byte swizzle.
+static bool gr_map(CUtensorMap* map, const void* base, unsigned long long rows, unsigned long long cols,
+                   unsigned box_rows) {
+  auto fn = gr_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t grouped_fp8_workspace_bytes() { return 256; }
+
+int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  if (workspace == nullptr || workspace_bytes < grouped_fp8_workspace_bytes())
+    return set_last_error(FME_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                          grouped_fp8_workspace_bytes());
+  if (g.R == 0) return FME_OK;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_last_error(FME_ECUDA, "cudaGetDevice failed");
+  const int sms = device_sm_count(dev);
+  if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
+  GrArgs a = {};
+  if (!gr_map(&a.mapg, g.a, g.a_rows, g.K, 1) ||
+      !gr_map(&a.mapw, g.w, static_cast<unsigned long long>(g.E) * g.N, g.K, 128))
+    return set_last_error(FME_ECUDA, "cuTensorMapEncodeTiled failed or unavailable");
+  a.sa = g.sa;
+  a.sw = g.sw;
+  a.offsets = g.offsets;
+  a.in_rows = g.in_rows;
+  a.out_rows = g.out_rows;
+  a.a_rows = g.a_rows;
+  a.R = g.R;
+  a.out_n = g.out_n;
+  a.K = g.K;
+  a.N = g.N;
+  a.E = g.E;
+  a.up0 = g.gate_first ? g.N / 2 : 0;
+  a.gate0 = g.gate_first ? 0 : g.N / 2;
+  a.limit = g.limit;
+  a.ue8m0 = g.ue8m0 ? 1 : 0;
+  a.q = g.q;
+  a.sq = g.sq;
+  a.out = static_cast<__nv_bfloat16*>(g.out);
+  a.err = static_cast<uint32_t*>(workspace);
+  a.timeout_ns = wait_timeout_ns();
+  const bool swiglu = g.q != nullptr;
+  const void* kernel = swiglu ? reinterpret_cast<const void*>(grouped_fp8_kernel<true>)
+                              : reinterpret_cast<const void*>(grouped_fp8_kernel<false>);
+  if (!ensure_smem_attr(dev, kernel, kGrSmemBytes)) return FME_ECUDA;
+  // No more CTAs than the most tiles these sizes can make (a group's last row tile may be part empty).
+  const long long n_tiles = swiglu ? g.N / 256 : (g.N + 255) / 256;
+  const long long most = (static_cast<long long>(g.R) / 128 + (g.R < g.E ? g.R : g.E)) * n_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
+  cfg.blockDim = dim3(kGrThreads);
+  cfg.dynamicSmemBytes = kGrSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = swiglu ? cudaLaunchKernelEx(&cfg, grouped_fp8_kernel<true>, a)
+                                 : cudaLaunchKernelEx(&cfg, grouped_fp8_kernel<false>, a);
+  if (err != cudaSuccess) return set_last_error(FME_ECUDA, "grouped fp8 launch: %s", cudaGetErrorString(err));
+  return FME_OK;
+}
+
+}  // namespace fme

@@ -84,6 +84,39 @@ int mxfp8_quantize(const void* x, int T, int H, uint8_t* q, uint8_t* scales, cud
 int combine_rmsnorm(const void* partials, int T, int N, int H, const void* gamma, float eps, void* latent,
                     void* normed, cudaStream_t st);
 
+// Residual addition, RMSNorm and 8-bit quantisation of x [T, H]: FP32 scales [T, H/128] or, with mxscales given,
+// E8M0 bytes [T, H/32]. residual / residual_out / normed may be null (arguments validated).
+int add_rmsnorm_quant(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T, int H,
+                      float eps, int ue8m0, uint8_t* q, float* scales, uint8_t* mxscales, void* normed,
+                      void* residual_out, cudaStream_t st);
+
+// Picks and weights of T tokens and their routes sorted by expert (arguments validated).
+size_t route_workspace_bytes(int T, int E);
+int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale, int32_t* ids,
+          float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace, size_t workspace_bytes,
+          cudaStream_t st);
+
+// A product grouped by expert (arguments validated): with q the SwiGLU
+// epilogue (N = 2I, q / sq written at the grouped row), else BF16 rows.
+struct GroupedFp8 {
+  const uint8_t* a = nullptr;
+  const float* sa = nullptr;
+  int a_rows = 0;
+  const uint8_t* w = nullptr;
+  const float* sw = nullptr;
+  const int32_t* offsets = nullptr;
+  const int32_t* in_rows = nullptr;
+  const int32_t* out_rows = nullptr;
+  int R = 0, out_n = 0, K = 0, N = 0, E = 0;
+  float limit = 0.0f;
+  int ue8m0 = 0, gate_first = 0;
+  uint8_t* q = nullptr;
+  float* sq = nullptr;
+  void* out = nullptr;
+};
+size_t grouped_fp8_workspace_bytes();
+int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cudaStream_t st);
+
 // Routing fused into the NVFP4 call: picks from logits + bias over E experts
 // (the routed FP8 rule), written to ids / weights [M, top_k].
 struct Nvfp4Routing {

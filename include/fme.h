@@ -365,6 +365,127 @@ int fme_moe_layer_nvfp4(const void* x, const void* logits, int logits_dtype, con
                         int e0, int top_k, float scale, float limit, void* y, int32_t* ids, float* weights,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Residual addition, RMSNorm and FP8 quantisation of T rows in one pass: the
+ * step before a prompt's routed experts (and before the router, through
+ * normed).
+ *
+ *   z = bf16(x + residual) (z = x without a residual)
+ *   y = z / sqrt(mean z^2 + eps) * gamma, in FP32
+ *   per 128 values: s = max(amax |y|, 1e-10) / 448 (rounded up to a power of
+ *   two when ue8m0), q = e4m3(y * (1 / s)): the x-quantisation of
+ *   "vllm.models.glm5next.nvidia.specialized_decode.mega_moe" (_MegaKernel's
+ *   epilogue), of the FP32 norm. The page's kernel is handed the BF16 norm;
+ *   quantising FP32 leaves out that rounding, so codes can differ by one
+ *   from quantising `normed`.
+ *
+ * Arguments: x [T, H] BF16, rows ldx elements apart; residual BF16, rows ldr
+ *   elements apart, or NULL; gamma [H] BF16; q [T, H] E4M3 bytes; scales
+ *   [T, H/128] FP32; normed [T, H] BF16 (y rounded) or NULL; residual_out
+ *   [T, H] BF16 (z), given exactly when residual is. residual_out may be
+ *   residual itself when its rows are dense (ldr = H); otherwise outputs must
+ *   not overlap inputs. 0 <= T <= 2^20 (0: nothing is done), H a multiple of
+ *   128 up to 16384, ldx and ldr multiples of 8 and >= H, eps finite and
+ *   >= 0. Every pointer 16-byte aligned. No workspace; asynchronous on
+ *   `stream` (PDL launch). Returns FME_OK, FME_EINVAL, FME_EALIGN or FME_ECUDA.
+ */
+int fme_add_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T,
+                        int H, float eps, int ue8m0, uint8_t* q, float* scales, void* normed, void* residual_out,
+                        void* stream);
+
+/*
+ * fme_add_rmsnorm_fp8 with MXFP8 output (the format fme_moe_routed_fp8_mx
+ * takes): per 32 values one E8M0 byte, exponent and rounding by
+ * fme_mxfp8_quantize's rule on the FP32 norm. H a multiple of 32 up to 16384;
+ * scales [T, H/32] bytes, any alignment. The rest as fme_add_rmsnorm_fp8.
+ */
+int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T,
+                          int H, float eps, uint8_t* q, uint8_t* scales, void* normed, void* residual_out,
+                          void* stream);
+
+/*
+ * Routing of T tokens, and the routes grouped by expert: what the grouped
+ * products below take.
+ *
+ * Source: "vllm.models.glm5next.nvidia.specialized_decode.mega_moe"
+ * (_MegaKernel.top_k_pick): the picks and weights of fme_moe_routed_fp8, bit
+ * for bit, for any T. The routes, numbered t * top_k + r, are sorted by
+ * expert, ascending within one expert.
+ *
+ * Arguments: logits [T, E] (logits_dtype FME_F32 or FME_BF16), bias [E] FP32,
+ *   scale finite. Outputs: ids [T, top_k] int32, weights [T, top_k] FP32,
+ *   offsets [E + 1] int32 (expert e holds places offsets[e] ..
+ *   offsets[e + 1] - 1; offsets[E] = T * top_k), rows [T * top_k] int32 (the
+ *   route at each place) and tokens [T * top_k] int32 (its token, route /
+ *   top_k). 0 <= T <= 2^20 (0: offsets are zeroed), E in [1, 1024], top_k in
+ *   [1, min(E, 32)]. NaN logits give picks that are distinct and in range.
+ *   Every pointer 16-byte aligned. The workspace (see
+ *   fme_moe_route_workspace) needs no zeroing. Errors: FME_OK, FME_EINVAL,
+ *   FME_EUNSUPPORTED, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA.
+ */
+int fme_moe_route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale,
+                  int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fme_moe_route needs for these sizes (0 on bad sizes). */
+size_t fme_moe_route_workspace(int T, int E, int top_k);
+
+/*
+ * Gate/up product, SwiGLU and FP8 re-quantisation of rows grouped by expert:
+ * GEMM1 of fme_moe_routed_fp8 for any number of tokens, on the same weights.
+ *
+ * Source: "vllm.models.glm5next.nvidia.specialized_decode.mega_moe" (GEMM1
+ * epilogue, hidden_block). For place p of group e (offsets[e] <= p <
+ * offsets[e + 1]), r = in_rows[p] (p without in_rows):
+ *   y[n] = sum_b (sum_{k in b} W13[e, n, k] a[r, k]) * (s13[e, n/128, b] * sa[r, b]);
+ *   h = silu(min(gate, limit)) * clamp(up, -limit, limit), in FP32;
+ *   per 128 values of h: scales = max(amax, 1e-10) / 448 (power of two when
+ *   ue8m0), q = e4m3(h / scale), written at place p.
+ *
+ * Arguments: a [a_rows, H] E4M3 and sa [a_rows, H/128] FP32 (as
+ *   fme_add_rmsnorm_fp8 writes them); w13 [E, 2I, H] E4M3 and s13
+ *   [E, 2I/128, H/128] FP32, up rows then gate rows (gate_first: gate rows
+ *   then up rows, the shared expert's order); offsets [E + 1] int32 ascending;
+ *   in_rows [R] int32 or NULL (then a_rows >= R); q [R, I] E4M3, scales
+ *   [R, I/128] FP32. R in [0, 2^25] (0: nothing is done), H a multiple of 128
+ *   up to 16384, I a multiple of 128 up to 8192, E in [1, 1024], a_rows in
+ *   [1, 2^25], limit > 0 (+inf allowed).
+ * Places no group holds are left as they are. Offsets are clamped to [0, R]
+ * on the device; an in_rows entry outside [0, a_rows) gives a row of zeros and
+ * sets error bit 8 of the workspace. Pointers 16-byte aligned (offsets and
+ * in_rows 4-byte). The workspace (fme_moe_grouped_fp8_workspace) must be
+ * zeroed before its first use. Errors as fme_moe_route.
+ */
+int fme_moe_grouped_swiglu_fp8(const uint8_t* a, const float* sa, int a_rows, const uint8_t* w13, const float* s13,
+                               const int32_t* offsets, const int32_t* in_rows, int R, int H, int I, int E, float limit,
+                               int ue8m0, int gate_first, uint8_t* q, float* scales, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Product of rows grouped by expert, BF16 rows out: GEMM2 of
+ * fme_moe_routed_fp8 for any number of tokens, on the same weights (source
+ * and arguments as fme_moe_grouped_swiglu_fp8).
+ *   out[out_rows[p], n] = bf16(sum_b (sum_{k in b} W[e, n, k] a[r, k]) * (sw[e, n/128, b] * sa[r, b]))
+ * with r = in_rows[p] and out_rows[p] each p when NULL. With out_rows =
+ * fme_moe_route's rows, out is in route order t * top_k + r and
+ * fme_moe_finalize combines it.
+ *
+ * Arguments: a [a_rows, K] E4M3, sa [a_rows, K/128] FP32, w [E, N, K] E4M3, sw
+ *   [E, N/128, K/128] FP32, out [out_n, N] BF16. K and N multiples of 128 up
+ *   to 16384, out_n in [1, 2^25] (>= R without out_rows). Output rows that no
+ *   place names are left as they are; an out_rows entry outside [0, out_n)
+ *   is skipped and sets error bit 8, as a bad in_rows entry does; two places
+ *   that name one row race.
+ */
+int fme_moe_grouped_gemm_fp8(const uint8_t* a, const float* sa, int a_rows, const uint8_t* w, const float* sw,
+                             const int32_t* offsets, const int32_t* in_rows, const int32_t* out_rows, int R, int K,
+                             int N, int E, void* out, int out_n, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Workspace bytes the two grouped products need (N weight rows per expert: 2I
+ * for the first; 0 on bad sizes). */
+size_t fme_moe_grouped_fp8_workspace(int R, int K, int N, int E);
+
 /* Zero a workspace (cudaMemsetAsync on stream). */
 int fme_workspace_clear(void* workspace, size_t workspace_bytes, void* stream);
 

@@ -1,0 +1,381 @@
+"""GPU checks of the prompt operators against the 64-bit oracle.
+
+Tolerances, from the arithmetic (u = 2^-24, the FP32 rounding):
+* norm: a thread sums at most 64 squares, 13 additions join them, so the mean is within 80 u and 1 / sqrt within
+  half that plus three roundings; with the two products y is within 64 u of the exact norm.
+* a product: a block's partial sum is an FP32 accumulation of exact products and the scaled partials are added one
+  after another: within (K/128 + 8) * 2 u of the sum of the terms' magnitudes.
+* SwiGLU: |silu'| <= 1.1 and |silu(g)| <= |g|; expf, the division and the products add at most 16 u of the result.
+* E4M3 holds a value within 2^-4 of it (2^-10 of the scale below 2^-6 of it), BF16 within 2^-8.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import codecs, prompt, quant, routing
+from oracle.ep_local import mx_exponent
+from oracle.finalize import finalize as oracle_finalize
+from oracle.moe_fp8 import clamped_swiglu
+from synth import workloads as W
+from tests.parity import assert_outputs, assert_routing
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def fme():
+    import fp4_moe_expert_gb300 as m
+    return m
+
+
+def _dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    return t if dtype is None else t.to(dtype)
+
+
+def _np(t):
+    return t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+# --------------------------------------------------------------------------- norm
+def _norm_inputs(T, H, seed, residual):
+    rng = np.random.default_rng(seed)
+    x = codecs.bf16_round((rng.normal(size=(T, H)) * np.exp2(rng.integers(-3, 4, size=(T, 1)))).astype(np.float32))
+    r = codecs.bf16_round((5 * rng.normal(size=(T, H))).astype(np.float32)) if residual else None
+    g = codecs.bf16_round(rng.uniform(-1.5, 1.5, size=H).astype(np.float32))
+    if T > 2:
+        x[1] = 0
+        if residual:
+            r[1] = 0
+    return x, r, g
+
+
+def _check_codes(codes, scale, y, err):
+    """Each code's value times its scale is y, saturated at 448 scales, rounded to E4M3 (err: how far the kernel's y
+    may be off). MXFP8's exponent leaves values between 448 and 512 scales to the saturation."""
+    v = codecs.e4m3_decode(codes) * scale
+    y = np.clip(y, -448 * scale, 448 * scale)
+    assert np.all(np.abs(v - y) <= np.maximum(np.abs(y) * 2.0 ** -4, scale * 2.0 ** -10) * 1.001 + err)
+
+
+@pytest.mark.parametrize("T,H,residual,ue8m0", [(1, 128, False, False), (1, 7168, True, False), (5, 1024, True, True),
+                                                (3, 1152, False, False), (67, 3584, True, False), (2, 8192, True, False),
+                                                (9, 16384, True, True), (300, 256, False, False)])
+def test_add_rmsnorm_fp8(fme, T, H, residual, ue8m0):
+    x, r, g = _norm_inputs(T, H, T + H, residual)
+    z, y = prompt.add_rmsnorm(x, r, g, 1e-5)
+    bf = torch.bfloat16
+    q, s, res, normed = fme.add_rmsnorm_fp8(_dev(x, bf), _dev(g, bf), None if r is None else _dev(r, bf), 1e-5, ue8m0,
+                                            want_normed=True)
+    assert (res is None) == (r is None)
+    if res is not None:
+        assert np.array_equal(_np(res), z)
+    assert np.all(np.abs(_np(normed) - y) <= np.abs(y) * 2.0 ** -8 * 1.001)
+    s = _np(s).astype(np.float64)
+    amax = np.abs(y).reshape(T, H // 128, 128).max(-1)
+    base = np.maximum(amax, 1e-10) / 448
+    if ue8m0:
+        base = np.maximum(base, 1e-10)
+        assert np.array_equal(s, np.exp2(np.round(np.log2(s))))
+        assert np.all(s >= base * (1 - 80 * U)) and np.all(s < 2 * base * (1 + 80 * U))
+    else:
+        assert np.all(np.abs(s - base) <= 70 * U * base)
+    _check_codes(_np(q), np.repeat(s, 128, axis=1), y, 70 * U * np.abs(y))
+
+
+@pytest.mark.parametrize("T,H,residual", [(1, 32, False), (4, 96, True), (33, 3584, True), (2, 7168, False),
+                                          (3, 8224, True)])
+def test_add_rmsnorm_mxfp8(fme, T, H, residual):
+    x, r, g = _norm_inputs(T, H, 3 * T + H, residual)
+    z, y = prompt.add_rmsnorm(x, r, g, 1e-5)
+    bf = torch.bfloat16
+    q, s, res, normed = fme.add_rmsnorm_mxfp8(_dev(x, bf), _dev(g, bf), None if r is None else _dev(r, bf), 1e-5)
+    assert normed is None
+    if r is not None:
+        assert np.array_equal(_np(res), z)
+    e = _np(s).astype(np.int64) - 127
+    amax = np.abs(y).reshape(T, H // 32, 32).max(-1)
+    low, high = (np.vectorize(mx_exponent)(amax * f) for f in (1 - 70 * U, 1 + 70 * U))
+    assert np.all((e >= low) & (e <= high))
+    _check_codes(_np(q), np.repeat(np.exp2(e.astype(np.float64)), 32, axis=1), y, 70 * U * np.abs(y))
+
+
+def test_norm_strides_in_place_and_streams(fme):
+    T, H = 37, 640
+    x, r, g = _norm_inputs(T, H, 5, True)
+    bf = torch.bfloat16
+    dx, dr, dg = _dev(x, bf), _dev(r, bf), _dev(g, bf)
+    ref = fme.add_rmsnorm_fp8(dx, dg, dr, want_normed=True)
+    wide = torch.full((T, H + 24), float("nan"), dtype=bf, device=DEV)
+    wide[:, 8:H + 8] = dx
+    rwide = torch.full((T, 2 * H), float("nan"), dtype=bf, device=DEV)
+    rwide[:, :H] = dr
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = fme.add_rmsnorm_fp8(wide[:, 8:H + 8], dg, rwide[:, :H], want_normed=True)
+        same = fme.add_rmsnorm_fp8(dx, dg, dr, want_normed=True, residual_out=dr)  # the residual updated in place
+    side.synchronize()
+    assert same[2] is dr
+    for a, b, c in zip(ref, got, same):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_norm_bad_values_stay_in_their_row(fme):
+    x, _, g = _norm_inputs(4, 512, 8, False)
+    bf = torch.bfloat16
+    dx, dg = _dev(x, bf), _dev(g, bf)
+    ref = fme.add_rmsnorm_fp8(dx, dg, want_normed=True)
+    bad = dx.clone()
+    bad[0, 5] = float("nan")
+    bad[2, 7] = float("inf")
+    got = fme.add_rmsnorm_fp8(bad, dg, want_normed=True)
+    for a, b in ((ref[0], got[0]), (ref[1], got[1]), (ref[3], got[3])):
+        assert torch.equal(a[1::2], b[1::2])
+    assert torch.isnan(got[3][0]).all()
+
+
+def test_norm_offsets_past_32_bits(fme):
+    H, ld, T = 256, 1 << 28, 10  # the last row starts 2.4e9 elements in
+    g = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    buf = torch.zeros((T - 1) * ld + H, dtype=torch.bfloat16, device=DEV)
+    x = buf.as_strided((T, H), (ld, 1))
+    x.copy_(torch.randn(T, H, device=DEV))
+    a = fme.add_rmsnorm_fp8(x, g)
+    b = fme.add_rmsnorm_fp8(x.contiguous(), g)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# --------------------------------------------------------------------------- route
+@pytest.mark.parametrize("T,E,k,bf16,spread", [(1, 256, 8, True, 0.05), (1, 8, 8, False, 0.1), (65, 40, 3, True, 0.1),
+                                               (333, 896, 16, False, 0.5), (2500, 256, 8, True, 0.05),
+                                               (200, 1024, 32, False, 0.1), (9, 1, 1, False, 0.1)])
+def test_route(fme, T, E, k, bf16, spread):
+    rng = np.random.default_rng(T + E)
+    logits = rng.normal(size=(T, E)).astype(np.float32)
+    if bf16:
+        logits = codecs.bf16_round(logits)
+    bias = rng.normal(size=E).astype(np.float32) * np.float32(spread)
+    dl = _dev(logits, torch.bfloat16 if bf16 else None)
+    ids, w, off, rows, tok = (_np(t) for t in fme.moe_route(dl, _dev(bias), k, 2.5))
+    rid, rw, keys = routing.route(logits, bias, k, 2.5)
+    assert_routing(ids, w, rid, rw, keys)
+    for got, ref in zip((off, rows, tok), prompt.group_routes(ids, E)):
+        assert np.array_equal(got, ref)
+
+
+def test_route_ties_go_to_the_lower_expert(fme):
+    T, E, k = 70, 48, 5
+    logits = torch.zeros(T, E, device=DEV)
+    logits[1::2, 40:43] = 1.0
+    ids, w, off, rows, _ = fme.moe_route(logits, torch.zeros(E, device=DEV), k)
+    assert ids[0].tolist() == [0, 1, 2, 3, 4] and ids[1].tolist() == [40, 41, 42, 0, 1]
+    assert np.array_equal(_np(rows), prompt.group_routes(_np(ids), E)[1])
+    assert torch.allclose(w.sum(1), torch.ones(T, device=DEV), atol=1e-6)
+
+
+def test_route_picks_match_the_decode_kernel(fme):
+    cfg, M = W.RAGGED, 33
+    w13h, w2h = W.fp8_weights_host(cfg, 3)
+    s13, s2 = W.fp8_weight_scales(cfg, 3)
+    x, logits, bias = W.fp8_activations(cfg, M, 4)
+    _, ids, w = fme.moe_routed_fp8(_dev(x, torch.bfloat16), _dev(logits), _dev(bias), _dev(w13h.full()), _dev(s13),
+                                   _dev(w2h.full()), _dev(s2), cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0)
+    got = fme.moe_route(_dev(logits), _dev(bias), cfg.top_k, cfg.scale)
+    assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+
+
+def test_route_of_bad_logits_and_of_no_tokens(fme):
+    T, E, k = 20, 40, 6
+    logits = torch.randn(T, E, device=DEV)
+    logits[3] = float("nan")
+    logits[4] = -float("nan")
+    logits[5] = -float("inf")
+    logits[6, ::2] = float("inf")
+    ids, _, off, rows, _ = fme.moe_route(logits, torch.zeros(E, device=DEV), k)
+    a = _np(ids)
+    assert a.min() >= 0 and a.max() < E and all(len(set(r)) == k for r in a.tolist())
+    assert np.array_equal(_np(rows), prompt.group_routes(a, E)[1])
+    assert a[6].tolist() == [0, 2, 4, 6, 8, 10]
+    ids, w, off, rows, tok = fme.moe_route(logits[:0], torch.zeros(E, device=DEV), k)
+    assert ids.shape == (0, k) and rows.numel() == 0 and not off.any()
+
+
+# --------------------------------------------------------------------------- grouped products
+def _grouped_inputs(counts, H, N, a_rows, seed, gather, ue8m0=False):
+    rng = np.random.default_rng(seed)
+    E, R = len(counts), int(sum(counts))
+    a, sa = quant.fp8_quant_mul(rng.normal(size=(a_rows, H)).astype(np.float32), ue8m0)
+    w = codecs.e4m3_encode(rng.normal(size=(E, N, H)).astype(np.float32))
+    sw = np.exp2(rng.uniform(-7, -3, size=(E, N // 128, H // 128))).astype(np.float32)
+    off = np.cumsum([0] + list(counts)).astype(np.int32)
+    idx = rng.integers(0, a_rows, size=R).astype(np.int32) if gather else None
+    return a, sa, w, sw, off, idx
+
+
+COUNTS = [([1], 1), ([3, 0, 1, 5], 2), ([128, 129, 0, 127], 3), ([0, 0, 300, 7, 0], 4), ([31, 33, 64, 2, 16, 17], 5),
+          ([513], 6)]
+
+
+@pytest.mark.parametrize("counts,seed", COUNTS)
+@pytest.mark.parametrize("K,N", [(128, 128), (384, 384), (1024, 512)])
+def test_grouped_gemm(fme, counts, seed, K, N):
+    R = sum(counts)
+    gather = seed % 2 == 0
+    a, sa, w, sw, off, idx = _grouped_inputs(counts, K, N, max(R, 1) if not gather else 50, seed * 100 + K, gather)
+    y, size = prompt.grouped_product(a, sa, w, sw, off, idx)
+    tol = (K // 128 + 8) * 2 * U * size
+    perm = np.random.default_rng(seed).permutation(R).astype(np.int32)
+    out = fme.moe_grouped_gemm_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off),
+                                   in_rows=None if idx is None else _dev(idx), out_rows=_dev(perm))
+    got = _np(out)[perm]
+    assert np.all(np.abs(got - y) <= tol + np.abs(y) * 2.0 ** -8 * 1.001)
+    again = fme.moe_grouped_gemm_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off),
+                                     in_rows=None if idx is None else _dev(idx))
+    assert np.array_equal(_np(again), got)
+
+
+@pytest.mark.parametrize("counts,seed", COUNTS)
+@pytest.mark.parametrize("H,I,limit,ue8m0,gate_first", [(128, 128, 7.0, False, False), (512, 384, 0.5, True, False),
+                                                        (1024, 256, float("inf"), False, True)])
+def test_grouped_swiglu(fme, counts, seed, H, I, limit, ue8m0, gate_first):
+    R = sum(counts)
+    gather = seed % 2 == 1
+    a, sa, w, sw, off, idx = _grouped_inputs(counts, H, 2 * I, max(R, 1) if not gather else 70, seed * 10 + H, gather)
+    y, size = prompt.grouped_product(a, sa, w, sw, off, idx)
+    up, gate = (y[:, I:], y[:, :I]) if gate_first else (y[:, :I], y[:, I:])
+    su, sg = (size[:, I:], size[:, :I]) if gate_first else (size[:, :I], size[:, I:])
+    h = clamped_swiglu(gate, up, limit)
+    du, dg = ((H // 128 + 8) * 2 * U * v for v in (su, sg))
+    g, u = np.minimum(gate, limit), np.clip(up, -limit, limit)
+    dh = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + 16 * U * np.abs(h)
+    q, s = fme.moe_grouped_swiglu_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off),
+                                      in_rows=None if idx is None else _dev(idx), limit=limit, ue8m0=ue8m0,
+                                      gate_first=gate_first)
+    q, s = _np(q), _np(s).astype(np.float64)
+    hb, db = (v.reshape(R, I // 128, 128) for v in (h, dh))
+    base = np.maximum(np.abs(hb).max(-1), 1e-10) / 448
+    slack = db.max(-1) / 448 + 4 * U * base
+    if ue8m0:
+        base = np.maximum(base, 1e-10)
+        assert np.array_equal(s, np.exp2(np.round(np.log2(s))))
+        assert np.all(s >= base - slack) and np.all(s < 2 * (base + slack))
+    else:
+        assert np.all(np.abs(s - base) <= slack)
+    _check_codes(q, np.repeat(s, 128, axis=1), h, dh + 4 * U * np.abs(h))
+
+
+def test_grouped_offsets_rows_and_errors(fme):
+    """Places outside every group stay as they are; offsets out of range are clamped; a bad index gives zeros or is
+    skipped, and is reported; NaN codes stay in their row."""
+    K, N = 256, 256
+    a, sa, w, sw, _, _ = _grouped_inputs([40, 40], K, N, 90, 9, False)
+    da, dsa, dw, dsw = _dev(a), _dev(sa), _dev(w), _dev(sw)
+    ws = fme.Workspace(fme.moe_grouped_fp8_workspace(90, K, N, 2), DEV)
+
+    def off(*v):
+        return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+    full = fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(0, 40, 80), workspace=ws)
+    out = torch.full((90, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(10, 40, 75), out=out, workspace=ws)
+    assert torch.equal(out[10:75], full[10:75]) and (out[:10] == 7).all() and (out[75:] == 7).all()
+    out.fill_(7.0)
+    fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(-5, 40, 100000), out=out, workspace=ws)
+    assert torch.equal(out[:80], full[:80])
+    fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(60, 20, 10), out=out, workspace=ws)  # descending: nothing
+    assert ws.error() == 0
+    idx = torch.arange(90, dtype=torch.int32, device=DEV)
+    idx[3], idx[50] = -1, 90
+    got = fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(0, 40, 80), in_rows=idx, workspace=ws)
+    assert ws.error() == 8
+    keep = [i for i in range(80) if i not in (3, 50)]
+    assert torch.equal(got[keep], full[keep]) and (got[3] == 0).all() and (got[50] == 0).all()
+    out.fill_(7.0)
+    fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, off(0, 40, 80), out_rows=idx, out=out, workspace=ws)
+    assert ws.error() == 8
+    assert torch.equal(out[keep], full[keep]) and (out[3] == 7).all() and (out[50] == 7).all()
+    q, s = fme.moe_grouped_swiglu_fp8(da, dsa, dw, dsw, off(0, 40, 80), in_rows=idx, limit=7.0, workspace=ws)
+    assert ws.error() == 8 and (q[3] == 0).all() and (s[3] > 0).all()
+    bad = da.clone()
+    bad[7] = 0x7F
+    got = fme.moe_grouped_gemm_fp8(bad, dsa, dw, dsw, off(0, 40, 80), workspace=ws)
+    keep = [i for i in range(80) if i != 7]
+    assert torch.equal(got[keep], full[keep]) and torch.isnan(got[7]).all() and ws.error() == 0
+
+
+def test_grouped_no_rows_and_far_output_rows(fme):
+    K, N = 128, 7168
+    a, sa, w, sw, off, _ = _grouped_inputs([3, 2], K, N, 5, 11, False)
+    args = (_dev(a), _dev(sa), _dev(w), _dev(sw))
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    assert fme.moe_grouped_gemm_fp8(*args, torch.zeros(3, dtype=torch.int32, device=DEV), in_rows=none).shape == (0, N)
+    ref = fme.moe_grouped_gemm_fp8(*args, _dev(off))
+    far = torch.zeros(620000, N, dtype=torch.bfloat16, device=DEV)  # 4.4e9 elements
+    rows = torch.tensor([619999, 0, 300000, 599999, 5], dtype=torch.int32, device=DEV)
+    fme.moe_grouped_gemm_fp8(*args, _dev(off), out_rows=rows, out=far)
+    assert torch.equal(far[rows.long()], ref)
+    assert int((far != 0).any(1).sum()) == 5
+
+
+# --------------------------------------------------------------------------- together
+def _layer(cfg, seed):
+    w13h, w2h = W.fp8_weights_host(cfg, seed)
+    s13, s2 = W.fp8_weight_scales(cfg, seed)
+    return [_dev(v) for v in (w13h.full(), s13, w2h.full(), s2)]
+
+
+def test_prompt_layer_matches_the_decode_layer(fme):
+    """The same tokens, quantised the same, through the decode kernel and the prompt operators: picks and weights bit
+    for bit, combined rows within the decode kernel's own tolerance of each other."""
+    cfg, M = W.RAGGED, 60
+    weights = _layer(cfg, 21)
+    x, logits, bias = W.fp8_activations(cfg, M, 22)
+    codes, sx = quant.fp8_quant_mul(x, cfg.ue8m0)
+    routed = (cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0)
+    out, ids, wts = fme.moe_routed_fp8(_dev(x, torch.bfloat16), _dev(logits), _dev(bias), *weights, *routed)
+    y, pid, pw = fme.moe_prompt_fp8(_dev(codes), _dev(sx), _dev(logits), _dev(bias), *weights, *routed)
+    assert torch.equal(ids, pid) and torch.equal(wts, pw)
+    assert_outputs(_np(y), _np(fme.moe_finalize(out, wts)), "prompt against decode")
+    assert np.array_equal(_np(fme.moe_finalize(out, wts)), oracle_finalize(_np(out), _np(wts)))
+
+
+def test_prompt_operators_in_a_graph(fme):
+    cfg, T = W.RAGGED, 150
+    w13, s13, w2, s2 = _layer(cfg, 31)
+    gamma = torch.ones(cfg.H, dtype=torch.bfloat16, device=DEV)
+    x = torch.randn(T, cfg.H, device=DEV).bfloat16()
+    logits = torch.randn(T, cfg.E, device=DEV)
+    bias = torch.zeros(cfg.E, device=DEV)
+    y = torch.empty(T, cfg.H, dtype=torch.bfloat16, device=DEV)
+    R = T * cfg.top_k
+    ws = [fme.Workspace(n, DEV) for n in (fme.moe_route_workspace(T, cfg.E, cfg.top_k),
+                                          fme.moe_grouped_fp8_workspace(R, cfg.H, 2 * cfg.I, cfg.E),
+                                          fme.moe_grouped_fp8_workspace(R, cfg.I, cfg.H, cfg.E))]
+
+    def step(y=None):
+        q, s, _, _ = fme.add_rmsnorm_fp8(x, gamma)
+        _, wt, off, rows, tok = fme.moe_route(logits, bias, cfg.top_k, cfg.scale, workspace=ws[0])
+        hq, sh = fme.moe_grouped_swiglu_fp8(q, s, w13, s13, off, in_rows=tok, limit=cfg.limit, workspace=ws[1])
+        out = fme.moe_grouped_gemm_fp8(hq, sh, w2, s2, off, out_rows=rows, workspace=ws[2])
+        return fme.moe_finalize(out, wt, y=y)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(y)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(y)
+    for _ in range(3):
+        x.normal_()
+        logits.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, step())
+    assert [w.error() for w in ws] == [0, 0, 0]
