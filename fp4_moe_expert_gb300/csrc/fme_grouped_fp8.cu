@@ -12,11 +12,12 @@
 // One persistent CTA per SM walks tiles of 128 rows of a group x 256 weight rows
 // (swiglu: the 128 up rows and the 128 gate rows of one 128-value hidden
 // block, so its quantisation block is inside the tile and one thread holds
-// both halves of a value). Ten warps: 0-7 accumulate, 8 loads, 9 issues the MMA.
-// * Loads: per 128-value K block two 128-row boxes of weights and the tile's rows
-//   gathered by TMA (tile::gather4, four rows a lane), only the rows the group
-//   has: a group of one row moves 512 bytes of activations beside its 32 KB of
-//   weights.
+// both halves of a value). Twelve warps: 0-7 accumulate, 8 loads by TMA, 9 issues
+// the MMA, 10-11 copy activation rows by index.
+// * Loads: per 128-value K block two 128-row boxes of weights by TMA, and the tile's
+//   rows: a full tile of consecutive rows as one box, others row by row with cp.async
+//   (only the rows the group has). TMA's own row gather (tile::gather4) measured
+//   90 clocks for four rows, 2900 a tile and K block against 512 of MMA work.
 // * The scales are FP32 and not powers of two, so the MMA cannot apply them: each
 //   K block is one 128 x 256 accumulation in tensor memory (two buffers), and the
 //   accumulate warps add D * (sw * sa) into 128 registers a thread. A row is a
@@ -31,16 +32,24 @@
 
 namespace fme {
 
-constexpr int kGrThreads = 320;
+constexpr int kGrThreads = 384;
+constexpr int kGrGatherThreads = 64;
+// Registers a thread: 384 x 168 at launch, then 8 accumulate warps x 216 and 4 others x 72 (the same sum).
+constexpr int kGrLaunchRegs = 168, kGrAccRegs = 216, kGrOtherRegs = 72;
+static_assert(2 * kGrAccRegs + kGrOtherRegs == 3 * kGrLaunchRegs, "register split");
 constexpr int kGrAccWarps = 8;
 constexpr int kGrStages = 4;
+// Scale slots. The producer fills slot it % 8 once the MMA of K block it - 4 is done, which waited for the
+// accumulate warps to leave K block it - 6: two slots to spare.
+constexpr int kGrSlots = 8;
 constexpr int kGrABytes = 128 * 128;
 constexpr int kGrBBytes = 256 * 128;
 constexpr int kGrStageBytes = kGrABytes + kGrBBytes;
 
 struct GrArgs {
-  CUtensorMap mapg;  // a as [a_rows, K bytes], box 1 row x 128 bytes (gather)
+  CUtensorMap mapa;  // a as [a_rows, K bytes], box 128 rows x 128 bytes (full tiles of consecutive rows)
   CUtensorMap mapw;  // weights as [E * N, K bytes], box 128 rows x 128 bytes
+  const uint8_t* a;
   const float* sa;
   const float* sw;
   const int32_t* offsets;
@@ -60,6 +69,7 @@ struct GrArgs {
 struct GrShared {
   uint64_t full[kGrStages], empty[kGrStages];
   uint64_t tfull[2], tempty[2];
+  uint64_t sfull[kGrSlots];
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -67,6 +77,8 @@ struct GrShared {
   int off[kMaxExperts + 1];     // group starts, clamped to [0, R] and ascending
   int tiles[kMaxExperts + 1];   // 128-row tiles before group e
   float amax[2][2][128];        // [tile parity][column half][row]
+  float sx[kGrSlots][128];      // activation scales of a K block's rows
+  float sw[kGrSlots][2];        // weight scales of its two 128-row boxes
 };
 
 constexpr size_t kGrSmemBytes = static_cast<size_t>(kGrStages) * kGrStageBytes + 1024 + sizeof(GrShared);
@@ -98,6 +110,13 @@ __device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles,
   return g;
 }
 
+// Row of a that place i of the tile reads (past its end: its last row's; a bad index: row 0, the result is dropped).
+__device__ __forceinline__ int gr_row(const GrArgs& a, const GrTile& g, int i) {
+  const int p = g.p0 + min(i, g.rows - 1);
+  const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
+  return r >= 0 && r < a.a_rows ? r : 0;
+}
+
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid_constant__ GrArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -109,13 +128,14 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 
   if (tid == 0) {
     for (int s = 0; s < kGrStages; ++s) {
-      mbar_init(&S.full[s], 1);
+      mbar_init(&S.full[s], 1 + kGrGatherThreads);
       mbar_init(&S.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S.tfull[b], 1);
       mbar_init(&S.tempty[b], kGrAccWarps);
     }
+    for (int s = 0; s < kGrSlots; ++s) mbar_init(&S.sfull[s], 32);
     mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
@@ -125,11 +145,11 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     tmem_relinquish();
   }
   if (warp == 8 && lane == 0) {
-    prefetch_tmap(&a.mapg);
+    prefetch_tmap(&a.mapa);
     prefetch_tmap(&a.mapw);
   }
   griddep_wait();
-  // Row tiles before each group: every thread four groups, then a block scan.
+  // Row tiles before each group: every thread a few groups, then a block scan.
   constexpr int kPer = (kMaxExperts + kGrThreads - 1) / kGrThreads;
   int own[kPer], sum = 0;
 #pragma unroll
@@ -167,6 +187,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   const int total = S.tiles[a.E] * n_tiles;
   const uint32_t tmem = S.tmem;
   const volatile int* abort = &S.abort;
+  if (warp >= kGrAccWarps) reg_dec<kGrOtherRegs>();
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
@@ -174,19 +195,17 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const GrTile g = gr_tile(S, a.E, n_tiles, t);
-      int4 y;
-      int* yp = &y.x;
+      const bool box = a.in_rows == nullptr && g.rows == 128;
+      const float* sa[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p = g.p0 + min(4 * lane + i, g.rows - 1);
-        const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
-        yp[i] = r >= 0 && r < a.a_rows ? r : 0;  // a bad row is read as row 0 and written as zeros
-      }
-      const bool gather = 4 * lane < g.rows;
+      for (int i = 0; i < 4; ++i) sa[i] = a.sa + static_cast<size_t>(gr_row(a, g, 4 * lane + i)) * KB;
+      // Lane i < 2: the scales of weight box i.
+      const int wb = SWIGLU ? (lane == 0 ? a.up0 : a.gate0) / 128 + g.n : min(2 * g.n + lane, a.N / 128 - 1);
+      const float* sw = a.sw + (static_cast<size_t>(g.e) * (a.N / 128) + wb) * KB;
       const int w0 = SWIGLU ? g.e * a.N + a.up0 + 128 * g.n : g.e * a.N + 256 * g.n;
       const int w1 = SWIGLU ? g.e * a.N + a.gate0 + 128 * g.n : w0 + 128;
       const bool two = SWIGLU || 256 * g.n + 128 < a.N;
-      const uint32_t bytes = 512u * ((g.rows + 3) / 4) + (two ? kGrBBytes : kGrBBytes / 2);
+      const uint32_t bytes = (box ? kGrABytes : 0) + (two ? kGrBBytes : kGrBBytes / 2);
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages;
         ok = mbar_wait(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
@@ -195,13 +214,19 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         uint8_t* st = ring + s * kGrStageBytes;
         if (lane == 0) mbar_arrive_expect_tx(&S.full[s], bytes);
         __syncwarp();
-        if (gather) tma_gather4(st + 512 * lane, &a.mapg, 128 * j, y, &S.full[s]);
         if (lane == 0) tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, w0, &S.full[s]);
+        if (lane == 2 && box) tma_load_2d(st, &a.mapa, 128 * j, g.p0, &S.full[s]);
         if (lane == 1 && two) tma_load_2d(st + kGrABytes + kGrBBytes / 2, &a.mapw, 128 * j, w1, &S.full[s]);
+        const uint32_t slot = it % kGrSlots;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async_4(&S.sx[slot][4 * lane + i], sa[i] + j);
+        if (lane < 2) cp_async_4(&S.sw[slot][lane], sw + j);
+        cp_async_arrive(&S.sfull[slot]);
       }
     }
     if (!ok) {
       // Copies in flight must land before the CTA leaves its shared memory.
+      cp_async_wait_all();
       if (lane == 0) {
         atomicOr(a.err, kErrRingWait);
         S.abort = 1;
@@ -221,6 +246,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           ok = mbar_wait(&S.tempty[b], ((it >> 1) & 1) ^ 1, a.timeout_ns, abort) &&
                mbar_wait(&S.full[s], (it / kGrStages) & 1, a.timeout_ns, abort);
           if (!ok) break;
+          fence_proxy_async_smem();  // the gather's cp.async writes, before the MMA reads them
           tc_fence_after();
           const uint32_t st = smem_u32(ring) + s * kGrStageBytes;
 #pragma unroll
@@ -239,12 +265,44 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       }
     }
     __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ activation rows by index
+    // Eight threads copy a row's 128 bytes, swizzled as the MMA's descriptor says.
+    const int gt = tid - 320, chunk = gt & 7, r0 = gt >> 3;
+    const uint32_t dst0 = r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      const bool box = a.in_rows == nullptr && g.rows == 128;
+      int row[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) row[i] = gr_row(a, g, r0 + 8 * i);
+      const int n = box ? 0 : (g.rows - r0 + 7) / 8;  // rows this thread copies
+      const uint8_t* src = a.a + 16 * chunk;
+      for (int j = 0; j < KB; ++j, ++it, src += 128) {
+        const uint32_t s = it % kGrStages;
+        ok = mbar_wait(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        if (!ok) break;
+        uint8_t* st = ring + s * kGrStageBytes + dst0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+        cp_async_arrive(&S.full[s]);
+      }
+    }
+    if (!ok) {
+      atomicOr(a.err, kErrRingWait);
+      S.abort = 1;
+    }
+    cp_async_wait_all();
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ accumulate and epilogue
+    reg_inc<kGrAccRegs>();
     const int half = warp >> 2, quad = warp & 3;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    const int wblocks = a.N / 128;  // 128-row weight blocks of one expert
     uint32_t it = 0;
     int parity = 0;
     bool ok = true;
@@ -255,32 +313,31 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const int p = g.p0 + min(row, g.rows - 1);
       const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
       const bool bad = r < 0 || r >= a.a_rows;
-      const float* sa = a.sa + static_cast<size_t>(bad ? 0 : r) * KB;
-      const int b0 = SWIGLU ? a.up0 / 128 + g.n : min(2 * g.n + half, wblocks - 1);
-      const int b1 = SWIGLU ? a.gate0 / 128 + g.n : b0;
-      const float* sw0 = a.sw + (static_cast<size_t>(g.e) * wblocks + b0) * KB;
-      const float* sw1 = a.sw + (static_cast<size_t>(g.e) * wblocks + b1) * KB;
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
       for (int j = 0; j < KB; ++j, ++it) {
-        const uint32_t b = it & 1;
-        const float sx = __ldg(sa + j);
-        const float s0 = __fmul_rn(__ldg(sw0 + j), sx), s1 = SWIGLU ? __fmul_rn(__ldg(sw1 + j), sx) : s0;
-        ok = ok && mbar_wait(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
+        const uint32_t b = it & 1, slot = it % kGrSlots;
+        ok = ok && mbar_wait(&S.sfull[slot], (it / kGrSlots) & 1, a.timeout_ns, abort) &&
+             mbar_wait(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
+        const float sx = S.sx[slot][row];
+        const float s0 = __fmul_rn(S.sw[slot][SWIGLU ? 0 : half], sx), s1 = SWIGLU ? __fmul_rn(S.sw[slot][1], sx) : s0;
         if (live) {
           tc_fence_after();
+          // Sixteen columns ahead: one load is in flight while the other's values are added.
+          const uint32_t base = lanes + 256 * b + (SWIGLU ? 64 : 128) * half;
+          float d[2][16];
+          tmem_ld_issue(base, d[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float d[32];
-            const uint32_t col = SWIGLU ? (c >> 1) * 128 + 64 * half + 32 * (c & 1) : 128 * half + 32 * c;
-            tmem_ld_issue(lanes + 256 * b + col, d);
-            tmem_ld_join(d);
-            const float s = c < 2 ? s0 : s1;
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_join(d[c & 1]);
+            if (c < 7) tmem_ld_issue(base + (SWIGLU && c >= 3 ? 64 : 0) + 16 * (c + 1), d[(c + 1) & 1]);
+            const float s = c < 4 ? s0 : s1;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(d[i], s, acc[32 * c + i]);
+            for (int i = 0; i < 16; i += 2)
+              fma2(acc[16 * c + i], acc[16 * c + i + 1], d[c & 1][i], d[c & 1][i + 1], s);
           }
           tc_fence_before();
         }
@@ -399,9 +456,10 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   const int sms = device_sm_count(dev);
   if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
   GrArgs a = {};
-  if (!gr_map(&a.mapg, g.a, g.a_rows, g.K, 1) ||
+  if (!gr_map(&a.mapa, g.a, g.a_rows, g.K, 128) ||
       !gr_map(&a.mapw, g.w, static_cast<unsigned long long>(g.E) * g.N, g.K, 128))
     return set_last_error(FME_ECUDA, "cuTensorMapEncodeTiled failed or unavailable");
+  a.a = g.a;
   a.sa = g.sa;
   a.sw = g.sw;
   a.offsets = g.offsets;

@@ -68,6 +68,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// 4-byte global -> shared copy.
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// This thread's arrival on an mbarrier (counted at its init) once every cp.async it issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Waits until every cp.async this thread issued has landed.
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -106,6 +114,16 @@ __device__ __forceinline__ bool named_bar_or(int id, int threads, bool pred) {
       : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(pred))
       : "memory");
   return r != 0;
+}
+
+// Registers per thread of the calling warpgroup, up (inc) or down (dec); every warp of it executes this.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ------------------------------------------------------------------ conversions
@@ -163,14 +181,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, 
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
       "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-// Four rows (y0 .. y3) of 128 bytes at byte column x into 512 bytes of shared memory; the map's box is one row high.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, int4 y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-      "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
       : "memory");
 }
 // tma_load_2d without a cache policy.
@@ -305,25 +315,28 @@ __device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// Thirty-two columns in flight until tmem_ld_join: the join names the registers, so nothing that uses
-// them can be scheduled above the wait.
-__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, float (&r)[32]) {
+// Sixteen columns in flight until tmem_ld_join: the join names the registers, so nothing that uses them can be
+// scheduled above the wait.
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
-        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
-        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_join(float (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_join(float (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
                  "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
-                 "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]),
-                 "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]),
-                 "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
+                 "+f"(r[15])::"memory");
+}
+// (a0, a1) += (d0, d1) * (s, s), two FP32 fused multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float d0, float d1, float s) {
+  asm("{ .reg .b64 a, d, t; mov.b64 a, {%0, %1}; mov.b64 d, {%2, %3}; mov.b64 t, {%4, %4}; fma.rn.f32x2 a, d, t, a; "
+      "mov.b64 {%0, %1}, a; }"
+      : "+f"(a0), "+f"(a1)
+      : "f"(d0), "f"(d1), "f"(s));
 }
 // Store sixteen 32-bit columns of this thread's TMEM lane (warp-wide, 32x32b shape).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
