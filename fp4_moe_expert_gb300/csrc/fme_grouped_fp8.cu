@@ -59,6 +59,7 @@ struct GrArgs {
   int up0, gate0;  // first up / gate weight row (swiglu)
   float limit;
   int ue8m0;
+  int wide;  // out is 32-byte aligned: whole sectors a store
   uint8_t* q;
   float* sq;
   __nv_bfloat16* out;
@@ -115,6 +116,34 @@ __device__ __forceinline__ int gr_row(const GrArgs& a, const GrTile& g, int i) {
   const int p = g.p0 + min(i, g.rows - 1);
   const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
   return r >= 0 && r < a.a_rows ? r : 0;
+}
+
+// h / s correctly rounded, from inv = 1 / s correctly rounded: one residual step on the product (Markstein 1990).
+// Exact for the quotients of a block, |h / s| <= 448; where a tiny h makes the residual underflow, the code is zero.
+__device__ __forceinline__ float quotient(float h, float s, float inv) {
+  const float q = __fmul_rn(h, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, h), inv, q);
+}
+// g / (1 + exp(-g)) with the decode kernel's roundings (expf, a rounded quotient), the reciprocal by a Newton step on
+// the hardware's approximation. Below -80, where the exact value is under 1e-33 and its E4M3 code zero, exp stays at
+// exp(80), so that no infinity meets the Newton step.
+__device__ __forceinline__ float silu(float g) {
+  const float d = __fadd_rn(1.0f, expf(fminf(-g, 80.0f)));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
+  return quotient(g, d, r);
+}
+// (lo, hi) rounded to BF16, lo in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 template <bool SWIGLU>
@@ -356,7 +385,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         for (int c = 0; c < 64; ++c) {
           const float up = fminf(fmaxf(acc[c], -a.limit), a.limit);
           const float gate = fminf(acc[64 + c], a.limit);
-          acc[c] = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
+          acc[c] = __fmul_rn(silu(gate), up);
           amax = fmaxf(amax, fabsf(acc[c]));
         }
         S.amax[parity][half][row] = amax;
@@ -369,11 +398,15 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           amax = fmaxf(amax, S.amax[parity][half ^ 1][row]);
           float s = __fdiv_rn(fmaxf(amax, 1e-10f), 448.0f);
           if (a.ue8m0) s = ue8m0_ceil(s);
+          const float inv = __fdiv_rn(1.0f, s);
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = f32x2_to_e4m3x2(__fdiv_rn(acc[4 * i], s), __fdiv_rn(acc[4 * i + 1], s)) |
-                   (f32x2_to_e4m3x2(__fdiv_rn(acc[4 * i + 2], s), __fdiv_rn(acc[4 * i + 3], s)) << 16);
+          for (int i = 0; i < 16; ++i) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = quotient(acc[4 * i + k], s, inv);
+            w[i] = f32x2_to_e4m3x2(v[0], v[1]) | (f32x2_to_e4m3x2(v[2], v[3]) << 16);
+          }
           const int I = a.N / 2;
           uint4* dst = reinterpret_cast<uint4*>(a.q + static_cast<size_t>(p) * I + 128 * g.n + 64 * half);
 #pragma unroll
@@ -387,17 +420,18 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           if (o < 0 || o >= a.out_n) {
             atomicOr(a.err, kErrRoute);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(o) * a.N + 256 * g.n + 128 * half);
+            __nv_bfloat16* dst = a.out + static_cast<size_t>(o) * a.N + 256 * g.n + 128 * half;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint32_t w[4];
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(acc[8 * i + 2 * k]));
-                const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(acc[8 * i + 2 * k + 1]));
-                w[k] = lo | (hi << 16);
+              for (int k = 0; k < 8; ++k) w[k] = bf16x2(acc[16 * i + 2 * k], acc[16 * i + 2 * k + 1]);
+              if (a.wide) {
+                st_global_32(dst + 16 * i, w);
+              } else {
+                reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
@@ -478,6 +512,7 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   a.q = g.q;
   a.sq = g.sq;
   a.out = static_cast<__nv_bfloat16*>(g.out);
+  a.wide = (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
   a.err = static_cast<uint32_t*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   const bool swiglu = g.q != nullptr;
