@@ -38,13 +38,14 @@ constexpr int kGrGatherThreads = 64;
 constexpr int kGrLaunchRegs = 168, kGrAccRegs = 216, kGrOtherRegs = 72;
 static_assert(2 * kGrAccRegs + kGrOtherRegs == 3 * kGrLaunchRegs, "register split");
 constexpr int kGrAccWarps = 8;
+// Scales travel in groups of up to four K blocks of a tile. The producer fills a group's slot once the MMA of the K block
+// four before its first is done, which waited for the accumulate warps to leave the K block two before that: the
+// groups still read are at most five back.
+constexpr int kGrSlots = 6;
+constexpr int kGrABytes = 128 * 128;    // 128 activation rows of a K block
+constexpr int kGrBoxBytes = 128 * 128;  // 128 weight rows
 constexpr int kGrStages = 4;
-// Scale slots. The producer fills slot it % 8 once the MMA of K block it - 4 is done, which waited for the
-// accumulate warps to leave K block it - 6: two slots to spare.
-constexpr int kGrSlots = 8;
-constexpr int kGrABytes = 128 * 128;
-constexpr int kGrBBytes = 256 * 128;
-constexpr int kGrStageBytes = kGrABytes + kGrBBytes;
+constexpr int kGrStageBytes = kGrABytes + 2 * kGrBoxBytes;
 
 struct GrArgs {
   CUtensorMap mapa;  // a as [a_rows, K bytes], box 128 rows x 128 bytes (full tiles of consecutive rows)
@@ -68,6 +69,8 @@ struct GrArgs {
 };
 
 struct GrShared {
+  float4 sx[kGrSlots][128];  // activation scales of the rows, four K blocks
+  float4 sw[kGrSlots][2];    // weight scales of the two 128-row boxes
   uint64_t full[kGrStages], empty[kGrStages];
   uint64_t tfull[2], tempty[2];
   uint64_t sfull[kGrSlots];
@@ -78,8 +81,6 @@ struct GrShared {
   int off[kMaxExperts + 1];     // group starts, clamped to [0, R] and ascending
   int tiles[kMaxExperts + 1];   // 128-row tiles before group e
   float amax[2][2][128];        // [tile parity][column half][row]
-  float sx[kGrSlots][128];      // activation scales of a K block's rows
-  float sw[kGrSlots][2];        // weight scales of its two 128-row boxes
 };
 
 constexpr size_t kGrSmemBytes = static_cast<size_t>(kGrStages) * kGrStageBytes + 1024 + sizeof(GrShared);
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
-    uint32_t it = 0;
+    uint32_t it = 0, group = 0;
+    const bool vec = KB % 4 == 0;  // rows of scales are whole 16-byte units
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const GrTile g = gr_tile(S, a.E, n_tiles, t);
@@ -231,26 +233,37 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       // Lane i < 2: the scales of weight box i.
       const int wb = SWIGLU ? (lane == 0 ? a.up0 : a.gate0) / 128 + g.n : min(2 * g.n + lane, a.N / 128 - 1);
       const float* sw = a.sw + (static_cast<size_t>(g.e) * (a.N / 128) + wb) * KB;
-      const int w0 = SWIGLU ? g.e * a.N + a.up0 + 128 * g.n : g.e * a.N + 256 * g.n;
-      const int w1 = SWIGLU ? g.e * a.N + a.gate0 + 128 * g.n : w0 + 128;
-      const bool two = SWIGLU || 256 * g.n + 128 < a.N;
-      const uint32_t bytes = (box ? kGrABytes : 0) + (two ? kGrBBytes : kGrBBytes / 2);
+      const int row0 = SWIGLU ? a.up0 + 128 * g.n : 256 * g.n, row1 = SWIGLU ? a.gate0 + 128 * g.n : row0 + 128;
+      const bool two = row1 < a.N;  // the last tile may have one box only
+      const uint32_t bytes = (box ? kGrABytes : 0) + (two ? 2 : 1) * kGrBoxBytes;
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages;
-        ok = mbar_wait(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes;
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[s], bytes);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&S.full[s], bytes);
+          tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, g.e * a.N + row0, &S.full[s]);
+          if (two) tma_load_2d(st + kGrABytes + kGrBoxBytes, &a.mapw, 128 * j, g.e * a.N + row1, &S.full[s]);
+          if (box) tma_load_2d(st, &a.mapa, 128 * j, g.p0, &S.full[s]);
+        }
         __syncwarp();
-        if (lane == 0) tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, w0, &S.full[s]);
-        if (lane == 2 && box) tma_load_2d(st, &a.mapa, 128 * j, g.p0, &S.full[s]);
-        if (lane == 1 && two) tma_load_2d(st + kGrABytes + kGrBBytes / 2, &a.mapw, 128 * j, w1, &S.full[s]);
-        const uint32_t slot = it % kGrSlots;
+        if ((j & 3) == 0) {
+          const uint32_t slot = group++ % kGrSlots;
+          if (vec) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async_4(&S.sx[slot][4 * lane + i], sa[i] + j);
-        if (lane < 2) cp_async_4(&S.sw[slot][lane], sw + j);
-        cp_async_arrive(&S.sfull[slot]);
+            for (int i = 0; i < 4; ++i) cp_async_l1_16(&S.sx[slot][4 * lane + i], sa[i] + j);
+            if (lane < 2) cp_async_l1_16(&S.sw[slot][lane], sw + j);
+          } else {
+            for (int k = 0; k < 4 && j + k < KB; ++k) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) cp_async_l1_4(&S.sx[slot][4 * lane + i].x + k, sa[i] + j + k);
+              if (lane < 2) cp_async_l1_4(&S.sw[slot][lane].x + k, sw + j + k);
+            }
+          }
+          cp_async_arrive(&S.sfull[slot]);
+        }
       }
     }
     if (!ok) {
@@ -260,38 +273,39 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         atomicOr(a.err, kErrRingWait);
         S.abort = 1;
         for (uint32_t k = it > kGrStages ? it - kGrStages : 0; k < it; ++k)
-          if (!mbar_wait(&S.full[k % kGrStages], (k / kGrStages) & 1, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
+          if (!mbar_wait_spin(&S.full[k % kGrStages], (k / kGrStages) & 1, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
       }
       __syncwarp();
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        for (int j = 0; j < KB; ++j, ++it) {
-          const uint32_t s = it % kGrStages, b = it & 1;
-          ok = mbar_wait(&S.tempty[b], ((it >> 1) & 1) ^ 1, a.timeout_ns, abort) &&
-               mbar_wait(&S.full[s], (it / kGrStages) & 1, a.timeout_ns, abort);
-          if (!ok) break;
-          fence_proxy_async_smem();  // the gather's cp.async writes, before the MMA reads them
-          tc_fence_after();
-          const uint32_t st = smem_u32(ring) + s * kGrStageBytes;
+    uint32_t it = 0;
+    bool ok = true;
+    const uint64_t desc0 = sw128_desc(smem_u32(ring));
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int j = 0; j < KB; ++j, ++it) {
+        const uint32_t s = it % kGrStages, b = it & 1;
+        ok = mbar_wait_spin2(&S.full[s], (it / kGrStages) & 1, &S.tempty[b], ((it >> 1) & 1) ^ 1, a.timeout_ns, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          // The start address is the descriptor's low field, in units of 16 bytes.
+          const uint64_t ad = desc0 + s * (kGrStageBytes >> 4), bd = ad + (kGrABytes >> 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc_mma_f8(tmem + 256 * b, sw128_desc(st + 32 * i), sw128_desc(st + kGrABytes + 32 * i), f8_idesc(128, 256),
-                      i != 0);
+          for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + 256 * b, ad + 2 * i, bd + 2 * i, f8_idesc(128, 256), i != 0);
           tc_commit(&S.empty[s]);
           tc_commit(&S.tfull[b]);
         }
+        __syncwarp();
       }
-      if (!ok) {
-        atomicOr(a.err, kErrRingWait);
-        S.abort = 1;
-        tc_commit(&S.drain);
-        if (!mbar_wait(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
-      }
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok && elect_one()) {
+      atomicOr(a.err, kErrRingWait);
+      S.abort = 1;
+      tc_commit(&S.drain);
+      if (!mbar_wait_spin(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
     }
     __syncwarp();
   } else if (warp >= 10) {
@@ -299,6 +313,13 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     // Eight threads copy a row's 128 bytes, swizzled as the MMA's descriptor says.
     const int gt = tid - 320, chunk = gt & 7, r0 = gt >> 3;
     const uint32_t dst0 = r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
+    // K block k's copies are waited for, and shown to the MMA, kLag K blocks later.
+    constexpr uint32_t kLag = 2;
+    auto land = [&](uint32_t k) {
+      cp_async_wait<kLag - 1>();
+      fence_proxy_async_smem();
+      mbar_arrive(&S.full[k % kGrStages]);
+    };
     uint32_t it = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -310,21 +331,25 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const int n = box ? 0 : (g.rows - r0 + 7) / 8;  // rows this thread copies
       const uint8_t* src = a.a + 16 * chunk;
       for (int j = 0; j < KB; ++j, ++it, src += 128) {
+        if (it >= kLag) land(it - kLag);
         const uint32_t s = it % kGrStages;
-        ok = mbar_wait(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes + dst0;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (i < n) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
-        cp_async_arrive(&S.full[s]);
+        cp_async_commit();
       }
     }
-    if (!ok) {
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    if (ok) {
+      for (uint32_t k = it > kLag ? it - kLag : 0; k < it; ++k) mbar_arrive(&S.full[k % kGrStages]);
+    } else {
       atomicOr(a.err, kErrRingWait);
       S.abort = 1;
     }
-    cp_async_wait_all();
     __syncwarp();
   } else {
     // ------------------------------------------------------------ accumulate and epilogue
@@ -332,7 +357,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     const int half = warp >> 2, quad = warp & 3;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    uint32_t it = 0;
+    // The MMA may write buffer b again.
+    auto release = [&](uint32_t b) {
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(&S.tempty[b]);
+    };
+    uint32_t it = 0, group = 0, slot = 0;
     int parity = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total; t += gridDim.x, parity ^= 1) {
@@ -346,13 +376,17 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
       for (int j = 0; j < KB; ++j, ++it) {
-        const uint32_t b = it & 1, slot = it % kGrSlots;
-        ok = ok && mbar_wait(&S.sfull[slot], (it / kGrSlots) & 1, a.timeout_ns, abort) &&
-             mbar_wait(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
+        const uint32_t b = it & 1;
+        if ((j & 3) == 0) {
+          slot = group % kGrSlots;
+          ok = ok && mbar_wait_spin(&S.sfull[slot], (group++ / kGrSlots) & 1, a.timeout_ns, abort);
+        }
+        ok = ok && mbar_wait_spin(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const float sx = S.sx[slot][row];
-        const float s0 = __fmul_rn(S.sw[slot][SWIGLU ? 0 : half], sx), s1 = SWIGLU ? __fmul_rn(S.sw[slot][1], sx) : s0;
+        const float sx = (&S.sx[slot][row].x)[j & 3];
+        const float s0 = __fmul_rn((&S.sw[slot][SWIGLU ? 0 : half].x)[j & 3], sx);
+        const float s1 = SWIGLU ? __fmul_rn((&S.sw[slot][1].x)[j & 3], sx) : s0;
         if (live) {
           tc_fence_after();
           // Sixteen columns ahead: one load is in flight while the other's values are added.
@@ -362,16 +396,19 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             tmem_ld_join(d[c & 1]);
-            if (c < 7) tmem_ld_issue(base + (SWIGLU && c >= 3 ? 64 : 0) + 16 * (c + 1), d[(c + 1) & 1]);
+            if (c < 7)
+              tmem_ld_issue(base + (SWIGLU && c >= 3 ? 64 : 0) + 16 * (c + 1), d[(c + 1) & 1]);
+            else
+              release(b);
             const float s = c < 4 ? s0 : s1;
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
               fma2(acc[16 * c + i], acc[16 * c + i + 1], d[c & 1][i], d[c & 1][i + 1], s);
           }
-          tc_fence_before();
+        } else {
+          __syncwarp();
+          release(b);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tempty[b]);
       }
       if (bad) {
         if (row < g.rows && half == 0) atomicOr(a.err, kErrRoute);
@@ -516,11 +553,8 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   a.err = static_cast<uint32_t*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   const bool swiglu = g.q != nullptr;
-  const void* kernel = swiglu ? reinterpret_cast<const void*>(grouped_fp8_kernel<true>)
-                              : reinterpret_cast<const void*>(grouped_fp8_kernel<false>);
-  if (!ensure_smem_attr(dev, kernel, kGrSmemBytes)) return FME_ECUDA;
-  // No more CTAs than the most tiles these sizes can make (a group's last row tile may be part empty).
   const long long n_tiles = swiglu ? g.N / 256 : (g.N + 255) / 256;
+  // No more CTAs than the most tiles these sizes can make (a group's last row tile may be part empty).
   const long long most = (static_cast<long long>(g.R) / 128 + (g.R < g.E ? g.R : g.E)) * n_tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
@@ -532,8 +566,9 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t err = swiglu ? cudaLaunchKernelEx(&cfg, grouped_fp8_kernel<true>, a)
-                                 : cudaLaunchKernelEx(&cfg, grouped_fp8_kernel<false>, a);
+  void (*kernel)(GrArgs) = swiglu ? grouped_fp8_kernel<true> : grouped_fp8_kernel<false>;
+  if (!ensure_smem_attr(dev, reinterpret_cast<const void*>(kernel), kGrSmemBytes)) return FME_ECUDA;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "grouped fp8 launch: %s", cudaGetErrorString(err));
   return FME_OK;
 }

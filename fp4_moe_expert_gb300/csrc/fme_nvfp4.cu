@@ -188,11 +188,6 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src, uint32_t s
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // UE4M3 scale byte of a group: e4m3(amax / 6), saturating ("nvfp4-megamoe-kernel
 // README.md" Bugs Found & Fixed 2: the stored scale is also the divisor).

@@ -68,9 +68,12 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// 4-byte global -> shared copy.
-__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+// 4- and 16-byte global -> shared copies through L1, for lines that are read in several steps.
+__device__ __forceinline__ void cp_async_l1_4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_l1_16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 // This thread's arrival on an mbarrier (counted at its init) once every cp.async it issued so far has landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -116,6 +119,46 @@ __device__ __forceinline__ bool named_bar_or(int id, int threads, bool pred) {
   return r != 0;
 }
 
+// mbar_wait for waits that are short and many: the timer is first read after 64 tries.
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                               const volatile int* abort) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (n % 64 == 0) {
+      if (abort != nullptr && *abort) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
+    }
+  }
+}
+// Both barriers' waits at once, so that their latencies overlap.
+__device__ __forceinline__ bool mbar_wait_spin2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                                                uint64_t limit_ns, const volatile int* abort) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p, q; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4; and.pred p, p, q; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+      : "memory");
+  return ok || (mbar_wait_spin(bar0, parity0, limit_ns, abort) && mbar_wait_spin(bar1, parity1, limit_ns, abort));
+}
+// Waits until at most N of this thread's committed cp.async groups are still in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// True in one lane of a converged warp. Around tensor-core and TMA instructions whose operands the whole warp holds
+// alike, so that they stay in uniform registers (a branch on the lane number makes each issue tens of clocks longer).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
 // Registers per thread of the calling warpgroup, up (inc) or down (dec); every warp of it executes this.
 template <int N>
 __device__ __forceinline__ void reg_inc() {
