@@ -97,12 +97,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a Stream object (2 us less a call); the public route where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != torch.Size(shape) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} contiguous={t.is_contiguous()} cuda={t.is_cuda}")
 
@@ -362,7 +368,7 @@ def _stream_workspace(nbytes, device, workspace):
     """The caller's workspace, or one kept per device, current stream and size."""
     if workspace is not None:
         return _workspace(nbytes, device, workspace)
-    key = (device, torch.cuda.current_stream(device).cuda_stream, nbytes)
+    key = (device.index, _stream(device), nbytes)
     ws = _ws_cache.get(key)
     if ws is None:
         ws = _ws_cache[key] = Workspace(nbytes, device)
@@ -370,7 +376,7 @@ def _stream_workspace(nbytes, device, workspace):
 
 
 def _rows(t, name):
-    """A BF16 CUDA matrix with dense rows, any row stride that is a multiple of 8."""
+    """Row stride of a BF16 CUDA matrix with contiguous rows."""
     if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected a CUDA bfloat16 matrix with contiguous rows, got {t.dtype} "
                          f"{tuple(t.shape)} strides={t.stride()} cuda={t.is_cuda}")
@@ -382,6 +388,10 @@ def _out(t, shape, dtype, device, name):
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, dtype, shape, name)
     return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _add_rmsnorm(x, gamma, residual, eps, mx, ue8m0, want_normed, q, scales, normed, residual_out):
@@ -397,20 +407,20 @@ def _add_rmsnorm(x, gamma, residual, eps, mx, ue8m0, want_normed, q, scales, nor
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     q = _out(q, (T, H), torch.uint8, dev, "q")
-    if mx:
-        scales = _out(scales, (T, H // 32), torch.uint8, dev, "scales")
-    else:
-        scales = _out(scales, (T, H // 128), torch.float32, dev, "scales")
+    scales = _out(scales, (T, H // (32 if mx else 128)), torch.uint8 if mx else torch.float32, dev, "scales")
     if want_normed or normed is not None:
         normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
     if T == 0:
         return q, scales, residual_out, normed
-    args = (_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), T, H, float(eps))
-    outs = (_ptr(q), _ptr(scales), _ptr(normed), _ptr(residual_out), _stream(dev))
     if mx:
-        _check(lib.fme_add_rmsnorm_mxfp8(*args, *outs))
+        st = lib.fme_add_rmsnorm_mxfp8(x.data_ptr(), ldx, _addr(residual), ldr, gamma.data_ptr(), T, H, eps,
+                                       q.data_ptr(), scales.data_ptr(), _addr(normed), _addr(residual_out),
+                                       _stream(dev))
     else:
-        _check(lib.fme_add_rmsnorm_fp8(*args, int(bool(ue8m0)), *outs))
+        st = lib.fme_add_rmsnorm_fp8(x.data_ptr(), ldx, _addr(residual), ldr, gamma.data_ptr(), T, H, eps,
+                                     int(bool(ue8m0)), q.data_ptr(), scales.data_ptr(), _addr(normed),
+                                     _addr(residual_out), _stream(dev))
+    _check(st)
     return q, scales, residual_out, normed
 
 

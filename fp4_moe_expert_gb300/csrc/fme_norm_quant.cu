@@ -7,16 +7,17 @@
 //   normed = bf16(y), residual_out = z
 //
 // HBM-bound: 2 (4 with a residual) bytes a value read, 1 to 5 written. Each row is
-// read once into registers, eight values a thread and chunk, by the fewest
-// warps that keep a thread at four chunks; a block's amax takes shuffles over its
-// 16 (4) threads.
+// read once, into registers as the BF16 values z are (16 registers a thread: four
+// chunks of eight values), by the fewest warps that hold it so; a block's amax takes
+// shuffles over its 16 (4) threads.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
 namespace fme {
 
-constexpr int kNqThreads = 256;
-constexpr int kNqWarps = kNqThreads / 32;
+constexpr int kNqChunks = 4;     // chunks of eight values a thread
+constexpr int kNqRowWarps = 16;  // most warps a row: 16384 values
+constexpr int kNqSmallRows = 8;  // rows a CTA, one a warp, where one warp holds a row
 
 struct NqArgs {
   const __nv_bfloat16* x;
@@ -50,70 +51,75 @@ __device__ __forceinline__ uint4 nq_pack(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// W warps a row, at most C chunks of eight values a thread.
-template <bool MX, int W, int C>
-__global__ void __launch_bounds__(kNqThreads) add_rmsnorm_quant_kernel(const NqArgs a) {
-  __shared__ float part[kNqWarps];
-  griddep_wait();
+// SMALL: a warp a row, kNqSmallRows a CTA; otherwise the CTA is the row's.
+template <bool MX, bool SMALL>
+__global__ void __launch_bounds__(SMALL ? 32 * kNqSmallRows : 32 * kNqRowWarps) add_rmsnorm_quant_kernel(const NqArgs a) {
+  __shared__ float part[kNqRowWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rt = threadIdx.x % (32 * W);  // thread of the row
-  const int t = blockIdx.x * (kNqWarps / W) + warp / W;
-  const bool live = t < a.T;
-  const int chunks = a.H / 8;
-  float z[C][8];
-  float total = 0.0f;
+  const int t = SMALL ? blockIdx.x * kNqSmallRows + warp : blockIdx.x;
+  const int rt = SMALL ? lane : threadIdx.x, width = SMALL ? 32 : blockDim.x;  // thread of the row, threads a row
+  const int chunks = t < a.T ? a.H / 8 : 0;
+  griddep_wait();
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.ldx);
+  uint4 z[kNqChunks];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int ch = rt + 32 * W * c;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) z[c][k] = 0.0f;
-    if (live && ch < chunks) nq_unpack(__ldg(reinterpret_cast<const uint4*>(a.x + t * a.ldx) + ch), z[c]);
+  for (int c = 0; c < kNqChunks; ++c) {
+    z[c] = make_uint4(0, 0, 0, 0);
+    if (rt + width * c < chunks) z[c] = __ldcs(x + rt + width * c);
   }
   if (a.residual != nullptr) {
+    const uint4* res = reinterpret_cast<const uint4*>(a.residual + t * a.ldr);
+    uint4* res_out = reinterpret_cast<uint4*>(a.residual_out + static_cast<size_t>(t) * a.H);
+    uint4 r[kNqChunks];
+    // residual_out may be the same buffer: this thread alone reads and writes these bytes.
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = rt + 32 * W * c;
-      if (live && ch < chunks) {
-        float r[8];
-        // residual_out may be the same buffer: a plain load, and this thread alone writes these bytes.
-        nq_unpack(*(reinterpret_cast<const uint4*>(a.residual + t * a.ldr) + ch), r);
+    for (int c = 0; c < kNqChunks; ++c)
+      if (rt + width * c < chunks) r[c] = __ldcs(res + rt + width * c);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = __fadd_rn(z[c][k], r[k]);
-        const uint4 zb = nq_pack(r);
-        nq_unpack(zb, z[c]);
-        *(reinterpret_cast<uint4*>(a.residual_out + static_cast<size_t>(t) * a.H) + ch) = zb;
+    for (int c = 0; c < kNqChunks; ++c)
+      if (rt + width * c < chunks) {
+        float v[8], w[8];
+        nq_unpack(z[c], v);
+        nq_unpack(r[c], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __fadd_rn(v[k], w[k]);
+        z[c] = nq_pack(v);
+        res_out[rt + width * c] = z[c];
       }
-    }
+  }
+  float total = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kNqChunks; ++c) {
+    float v[8];
+    nq_unpack(z[c], v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) total = __fmaf_rn(v[k], v[k], total);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) total = __fmaf_rn(z[c][k], z[c][k], total);
-#pragma unroll
   for (int d = 16; d >= 1; d >>= 1) total = __fadd_rn(total, __shfl_xor_sync(0xFFFFFFFFu, total, d));
-  if (W > 1) {
+  if (!SMALL) {
     if (lane == 0) part[warp] = total;
     __syncthreads();
     total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) total = __fadd_rn(total, part[warp / W * W + w]);
+    for (int w = 0; w < width / 32; ++w) total = __fadd_rn(total, part[w]);
   }
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(total, static_cast<float>(a.H)), a.eps)));
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int ch = rt + 32 * W * c;
-    const bool mine = live && ch < chunks;
-    float amax = 0.0f;
+  for (int c = 0; c < kNqChunks; ++c) {
+    const int ch = rt + width * c;
+    const bool mine = ch < chunks;
+    float amax = 0.0f, y[8];
     if (mine) {
       float g[8];
+      nq_unpack(z[c], y);
       nq_unpack(__ldg(reinterpret_cast<const uint4*>(a.gamma) + ch), g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        z[c][k] = __fmul_rn(__fmul_rn(z[c][k], rstd), g[k]);
-        amax = fmaxf(amax, fabsf(z[c][k]));
+        y[k] = __fmul_rn(__fmul_rn(y[k], rstd), g[k]);
+        amax = fmaxf(amax, fabsf(y[k]));
       }
       if (a.normed != nullptr)
-        *(reinterpret_cast<uint4*>(a.normed + static_cast<size_t>(t) * a.H) + ch) = nq_pack(z[c]);
+        *(reinterpret_cast<uint4*>(a.normed + static_cast<size_t>(t) * a.H) + ch) = nq_pack(y);
     }
     // A block's chunks lie in neighbouring lanes and are all inside or all past the row's end.
 #pragma unroll
@@ -134,35 +140,27 @@ __global__ void __launch_bounds__(kNqThreads) add_rmsnorm_quant_kernel(const NqA
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      w[k] = f32x2_to_e4m3x2(__fmul_rn(z[c][4 * k], inv), __fmul_rn(z[c][4 * k + 1], inv)) |
-             (f32x2_to_e4m3x2(__fmul_rn(z[c][4 * k + 2], inv), __fmul_rn(z[c][4 * k + 3], inv)) << 16);
+      w[k] = f32x2_to_e4m3x2(__fmul_rn(y[4 * k], inv), __fmul_rn(y[4 * k + 1], inv)) |
+             (f32x2_to_e4m3x2(__fmul_rn(y[4 * k + 2], inv), __fmul_rn(y[4 * k + 3], inv)) << 16);
     *(reinterpret_cast<uint2*>(a.q + static_cast<size_t>(t) * a.H) + ch) = make_uint2(w[0], w[1]);
   }
 }
 
-template <bool MX, int W, int C>
+template <bool MX>
 static cudaError_t nq_launch(const NqArgs& a, cudaStream_t st) {
-  constexpr int rows = kNqWarps / W;
+  const int warps = (a.H / 8 + 32 * kNqChunks - 1) / (32 * kNqChunks);
+  const bool small = warps == 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.T + rows - 1) / rows));
-  cfg.blockDim = dim3(kNqThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(small ? (a.T + kNqSmallRows - 1) / kNqSmallRows : a.T));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * (small ? kNqSmallRows : warps)));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, add_rmsnorm_quant_kernel<MX, W, C>, a);
-}
-
-template <bool MX>
-static cudaError_t nq_dispatch(const NqArgs& a, cudaStream_t st) {
-  const int chunks = a.H / 8;
-  if (chunks <= 128) return nq_launch<MX, 1, 4>(a, st);
-  if (chunks <= 256) return nq_launch<MX, 2, 4>(a, st);
-  if (chunks <= 512) return nq_launch<MX, 4, 4>(a, st);
-  if (chunks <= 1024) return nq_launch<MX, 8, 4>(a, st);
-  return nq_launch<MX, 8, 8>(a, st);
+  return small ? cudaLaunchKernelEx(&cfg, add_rmsnorm_quant_kernel<MX, true>, a)
+               : cudaLaunchKernelEx(&cfg, add_rmsnorm_quant_kernel<MX, false>, a);
 }
 
 int add_rmsnorm_quant(const void* x, long long ldx, const void* residual, long long ldr, const void* gamma, int T, int H,
@@ -183,7 +181,7 @@ int add_rmsnorm_quant(const void* x, long long ldx, const void* residual, long l
   a.mxscales = mxscales;
   a.normed = static_cast<__nv_bfloat16*>(normed);
   a.residual_out = static_cast<__nv_bfloat16*>(residual_out);
-  const cudaError_t err = mxscales != nullptr ? nq_dispatch<true>(a, st) : nq_dispatch<false>(a, st);
+  const cudaError_t err = mxscales != nullptr ? nq_launch<true>(a, st) : nq_launch<false>(a, st);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "add rmsnorm launch: %s", cudaGetErrorString(err));
   return FME_OK;
 }
