@@ -464,8 +464,9 @@ def moe_route(logits, bias, top_k, scale=1.0, ids=None, weights=None, offsets=No
         return ids, weights, offsets.zero_(), rows, tokens
     ws = _stream_workspace(moe_route_workspace(T, E, top_k), dev, workspace)
     ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
-    _check(lib.fme_moe_route(_ptr(logits), ldt, _ptr(bias), T, E, top_k, float(scale), _ptr(ids), _ptr(weights),
-                             _ptr(offsets), _ptr(rows), _ptr(tokens), ws.ptr(), ws.nbytes, _stream(dev)))
+    _check(lib.fme_moe_route(logits.data_ptr(), ldt, bias.data_ptr(), T, E, top_k, scale, ids.data_ptr(),
+                             weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), tokens.data_ptr(),
+                             ws.buf.data_ptr(), ws.nbytes, _stream(dev)))
     return ids, weights, offsets, rows, tokens
 
 
@@ -505,10 +506,10 @@ def moe_grouped_swiglu_fp8(a, sa, w13, s13, offsets, in_rows=None, limit=float("
     if R == 0:
         return q, scales
     ws = _stream_workspace(moe_grouped_fp8_workspace(R, H, two_i, E), dev, workspace)
-    _check(lib.fme_moe_grouped_swiglu_fp8(_ptr(a), _ptr(sa), a_rows, _ptr(w13), _ptr(s13), _ptr(offsets),
-                                          _ptr(in_rows), R, H, I, E, float(limit), int(bool(ue8m0)),
-                                          int(bool(gate_first)), _ptr(q), _ptr(scales), ws.ptr(), ws.nbytes,
-                                          _stream(dev)))
+    _check(lib.fme_moe_grouped_swiglu_fp8(a.data_ptr(), sa.data_ptr(), a_rows, w13.data_ptr(), s13.data_ptr(),
+                                          offsets.data_ptr(), _addr(in_rows), R, H, I, E, limit, int(bool(ue8m0)),
+                                          int(bool(gate_first)), q.data_ptr(), scales.data_ptr(), ws.buf.data_ptr(),
+                                          ws.nbytes, _stream(dev)))
     return q, scales
 
 
@@ -526,9 +527,9 @@ def moe_grouped_gemm_fp8(a, sa, w, sw, offsets, in_rows=None, out_rows=None, out
     if R == 0:
         return out
     ws = _stream_workspace(moe_grouped_fp8_workspace(R, K, N, E), dev, workspace)
-    _check(lib.fme_moe_grouped_gemm_fp8(_ptr(a), _ptr(sa), a_rows, _ptr(w), _ptr(sw), _ptr(offsets), _ptr(in_rows),
-                                        _ptr(out_rows), R, K, N, E, _ptr(out), out.shape[0], ws.ptr(), ws.nbytes,
-                                        _stream(dev)))
+    _check(lib.fme_moe_grouped_gemm_fp8(a.data_ptr(), sa.data_ptr(), a_rows, w.data_ptr(), sw.data_ptr(),
+                                        offsets.data_ptr(), _addr(in_rows), _addr(out_rows), R, K, N, E,
+                                        out.data_ptr(), out.shape[0], ws.buf.data_ptr(), ws.nbytes, _stream(dev)))
     return out
 
 

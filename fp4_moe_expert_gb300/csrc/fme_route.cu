@@ -1,14 +1,14 @@
-// Routing of any number of tokens, and the routes grouped by expert.
+// Routing of any number of tokens, and the routes grouped by expert, in one launch.
 //
 // Per token ("mega_moe" _MegaKernel.top_k_pick, as route_topk): s = sigmoid(logits), key = s + bias, the top_k
 // largest keys (ties: lower expert), weights s / (sum of the picked s) * scale. The T * top_k routes, numbered
 // t * top_k + r, are then sorted by expert, ascending within one: a counting sort.
 //
-// The tokens are cut into contiguous shares, one a CTA, and a CTA's share into contiguous
-// runs, one a warp, so counts per (CTA, warp, expert) give every route its place
-// without an order-dependent atomic.
-//   1  route_pick_kernel     picks, weights, and the CTA's routes per expert -> counts[CTA][E]
-//   2  route_place_kernel    expert starts from all counts, then each route to its place
+// The tokens are cut into contiguous shares, one a CTA, and a share into contiguous runs, one a warp. A warp picks
+// for its run and counts its routes per expert in shared memory; the CTAs publish their counts, meet once (bounded
+// wait), and each derives the expert starts and its own places from all counts. So every route has its place without
+// an atomic whose order could show.
+// Bound by latency: a pick round is a warp maximum and one lane's search for its next best.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
@@ -17,65 +17,94 @@ namespace fme {
 constexpr int kRtWarps = 16;
 constexpr int kRtThreads = 32 * kRtWarps;
 constexpr int kRtMaxCtas = 152;
+constexpr int kRtTokens = 16;  // least tokens a CTA is given, where there are as many
 
 struct RtArgs {
   const void* logits;
   const float* bias;
-  int logits_f32, T, E, top_k;
+  int logits_f32, vec, T, E, top_k;
   float scale;
   int per_cta, per_warp;  // tokens
+  int pitch;              // experts in a row of counts: E rounded up to 8
   int32_t* ids;
   float* weights;
   int32_t* offsets;
   int32_t* rows;
   int32_t* tokens;
-  uint16_t* counts;  // [CTAs][E]: a share holds fewer than 65,536 tokens
+  uint16_t* counts;  // [CTAs][pitch]: a share holds fewer than 65,536 tokens, an expert at most one route of each
+  uint32_t* err;
+  uint32_t* sync;  // CTAs arrived, CTAs past the wait; zero between calls
+  unsigned long long timeout_ns;
 };
 
-// The picks of token t: lane r < top_k gets rank r's expert and weight. Lane l holds experts l + 32 j.
+__device__ __forceinline__ float rt_sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
+__device__ __forceinline__ float rt_logit(const RtArgs& a, size_t i) {
+  return a.logits_f32 ? __ldg(static_cast<const float*>(a.logits) + i)
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[i]);
+}
+
+// The logits of experts J * lane .. J * lane + J - 1 of token t (J a multiple of 8: in 16-byte loads where rows allow).
 template <int J>
-__device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J], int t, int lane, int& my_e, float& my_w) {
-  float sc[J];
-  uint32_t ky[J];
+__device__ __forceinline__ void rt_load(const RtArgs& a, int t, int lane, float (&l)[J]) {
+  const size_t row = static_cast<size_t>(t) * a.E;
+  const int e0 = J * lane;
+  if (J >= 8 && a.vec) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane + 32 * j;
-    sc[j] = 0.0f;
-    if (e < a.E)
-      sc[j] = a.logits_f32
-                  ? __ldg(static_cast<const float*>(a.logits) + static_cast<size_t>(t) * a.E + e)
-                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[static_cast<size_t>(t) * a.E + e]);
+    for (int j = 0; j < J; j += 8)
+      if (e0 + j < a.E) {
+        if (a.logits_f32) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0 + j);
+          const float4 p = __ldg(src), q = __ldg(src + 1);
+          l[j] = p.x, l[j + 1] = p.y, l[j + 2] = p.z, l[j + 3] = p.w;
+          l[j + 4] = q.x, l[j + 5] = q.y, l[j + 6] = q.z, l[j + 7] = q.w;
+        } else {
+          const uint4 p =
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) + row + e0 + j));
+          const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            l[j + 2 * k] = __uint_as_float(w[k] << 16);
+            l[j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+          }
+        }
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (e0 + j < a.E) l[j] = rt_logit(a, row + e0 + j);
   }
+}
+
+// The picks of token t: lane r < top_k gets rank r's expert and weight.
+template <int J>
+__device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J], const float (&l)[J], int t, int lane,
+                                        int& my_e, float& my_w) {
+  uint32_t ky[J];
   uint32_t best = 0u;
   int best_j = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    sc[j] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-sc[j])));
     // At least 1, so that an expert (a NaN key, too) always stands above a lane's empty places.
-    ky[j] = (lane + 32 * j < a.E) ? max(1u, ordered_key(__fadd_rn(sc[j], bias[j]))) : 0u;
+    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(__fadd_rn(rt_sigmoid(l[j]), bias[j]))) : 0u;
     if (ky[j] > best) {
       best = ky[j];
       best_j = j;
     }
   }
-  float total = 0.0f, mine = 0.0f;
-  int mine_e = 0;
+  int mine = 0;
 #pragma unroll 1
   for (int r = 0; r < a.top_k; ++r) {
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t cand = best == top ? static_cast<uint32_t>(lane + 32 * best_j) : 0xFFFFFFFFu;
-    const int win = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, cand));
-    float sv = 0.0f;
-    if (lane == (win & 31)) {
-      // Only the winner's lane takes its pick out and looks for its next best.
+    // Lower lanes hold lower experts, and a lane's best is its lowest of equals.
+    const int win = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;
+    const int e = __shfl_sync(0xFFFFFFFFu, J * lane + best_j, win);
+    if (lane == r) mine = e;
+    if (lane == win) {
       best = 0u;
       int next = 0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (j == best_j) {
-          sv = sc[j];
-          ky[j] = 0u;
-        }
+        if (j == best_j) ky[j] = 0u;
         if (ky[j] > best) {
           best = ky[j];
           next = j;
@@ -83,109 +112,140 @@ __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J],
       }
       best_j = next;
     }
-    const float s = __shfl_sync(0xFFFFFFFFu, sv, win & 31);
-    total = __fadd_rn(total, s);
-    if (lane == r) {
-      mine = s;
-      mine_e = win;
-    }
   }
-  my_e = mine_e;
-  my_w = __fmul_rn(__fdiv_rn(mine, total), a.scale);
+  const float s = lane < a.top_k ? rt_sigmoid(rt_logit(a, static_cast<size_t>(t) * a.E + mine)) : 0.0f;
+  float total = 0.0f;
+  for (int r = 0; r < a.top_k; ++r) total = __fadd_rn(total, __shfl_sync(0xFFFFFFFFu, s, r));
+  my_e = mine;
+  my_w = __fmul_rn(__fdiv_rn(s, total), a.scale);
 }
 
 template <int J>
-__global__ void __launch_bounds__(kRtThreads) route_pick_kernel(const RtArgs a) {
-  __shared__ int hist[kMaxExperts];
+__global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
+  __shared__ uint16_t seen[kRtWarps][kMaxExperts];  // routes of a warp's run per expert, then its next place
+  __shared__ int all[kMaxExperts], prev[kMaxExperts];  // routes of every CTA, and of those before this one
+  __shared__ int start[kMaxExperts];                   // where this CTA's routes of an expert go
+  __shared__ int warp_sum[kRtWarps];
+  __shared__ int gave_up;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = gridDim.x;
+  for (int e = lane; e < a.E; e += 32) seen[warp][e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kRtThreads) all[e] = prev[e] = 0;
+  if (threadIdx.x == 0) gave_up = 0;
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kRtThreads) hist[e] = 0;
-  float bias[J];
+  const int c0 = min(a.T, static_cast<int>(blockIdx.x) * a.per_cta), c1 = min(a.T, c0 + a.per_cta);
+  const int t0 = min(c1, c0 + warp * a.per_warp), t1 = min(c1, t0 + a.per_warp);
+  if (t0 < t1) {
+    float bias[J], l[J], next[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) bias[j] = lane + 32 * j < a.E ? __ldg(a.bias + lane + 32 * j) : 0.0f;
-  __syncthreads();
-  const int c0 = blockIdx.x * a.per_cta, c1 = min(a.T, c0 + a.per_cta);
-  const int t0 = c0 + warp * a.per_warp, t1 = min(c1, t0 + a.per_warp);
-  for (int t = t0; t < t1; ++t) {
-    int e;
-    float w;
-    rt_pick<J>(a, bias, t, lane, e, w);
-    if (lane < a.top_k) {
-      a.ids[static_cast<size_t>(t) * a.top_k + lane] = e;
-      a.weights[static_cast<size_t>(t) * a.top_k + lane] = w;
-      atomicAdd(&hist[e], 1);
+    for (int j = 0; j < J; ++j) {
+      bias[j] = J * lane + j < a.E ? __ldg(a.bias + J * lane + j) : 0.0f;
+      l[j] = next[j] = 0.0f;
+    }
+    rt_load<J>(a, t0, lane, l);
+    __syncwarp();
+    for (int t = t0; t < t1; ++t) {
+      if (t + 1 < t1) rt_load<J>(a, t + 1, lane, next);
+      int e;
+      float w;
+      rt_pick<J>(a, bias, l, t, lane, e, w);
+      if (lane < a.top_k) {
+        a.ids[static_cast<size_t>(t) * a.top_k + lane] = e;
+        a.weights[static_cast<size_t>(t) * a.top_k + lane] = w;
+        ++seen[warp][e];  // a token's picks are distinct: its lanes never meet on one counter
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < J; ++j) l[j] = next[j];
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kRtThreads)
-    a.counts[static_cast<size_t>(blockIdx.x) * a.E + e] = static_cast<uint16_t>(hist[e]);
-}
-
-__global__ void __launch_bounds__(kRtThreads) route_place_kernel(const RtArgs a) {
-  __shared__ int start[kMaxExperts];              // where this CTA's routes of an expert go
-  __shared__ uint16_t before[kRtWarps][kMaxExperts];  // this warp's next place among them
-  __shared__ int warp_sum[kRtWarps];
-  griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = gridDim.x;
-  // Two experts a thread: routes of all CTAs, and of those before this one.
-  int all[2], prev[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
-    all[i] = prev[i] = 0;
+  for (int e = threadIdx.x; e < a.pitch; e += kRtThreads) {
+    int sum = 0;
     if (e < a.E)
-#pragma unroll 8
-      for (int c = 0; c < G; ++c) {
-        const int n = a.counts[static_cast<size_t>(c) * a.E + e];
-        all[i] += n;
-        prev[i] += c < static_cast<int>(blockIdx.x) ? n : 0;
+      for (int w = 0; w < kRtWarps; ++w) {
+        const int n = seen[w][e];
+        seen[w][e] = static_cast<uint16_t>(sum);
+        sum += n;
       }
+    if (G > 1)
+      a.counts[static_cast<size_t>(blockIdx.x) * a.pitch + e] = static_cast<uint16_t>(sum);
+    else if (e < a.E)
+      all[e] = sum;
   }
-  int scan = all[0] + all[1];
+  if (G > 1) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      red_release_gpu_add(a.sync, 1u);
+      const uint64_t begin = globaltimer_ns();
+      while (ld_acquire_gpu(a.sync) < static_cast<uint32_t>(G))
+        if (globaltimer_ns() - begin > a.timeout_ns) {
+          atomicOr(a.err, kErrCrossWait);
+          gave_up = 1;
+          break;
+        }
+      // The last CTA past the wait leaves both words zero for the next call.
+      if (!gave_up && atomicAdd(a.sync + 1, 1u) == static_cast<uint32_t>(G) - 1u) {
+        a.sync[0] = 0u;
+        a.sync[1] = 0u;
+      }
+    }
+    __syncthreads();
+    if (gave_up) return;
+    // Eight experts a load; the CTAs' rows are dealt to as many threads as there are to a column.
+    const int words = a.pitch / 8, lanes = kRtThreads / words, col = threadIdx.x % words, first = threadIdx.x / words;
+    if (first < lanes) {
+      int sum[8], sum_prev[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = sum_prev[k] = 0;
+#pragma unroll 4
+      for (int c = first; c < G; c += lanes) {
+        const uint4 p = __ldcg(reinterpret_cast<const uint4*>(a.counts + static_cast<size_t>(c) * a.pitch) + col);
+        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+        const bool before = c < static_cast<int>(blockIdx.x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int n = (w[k / 2] >> (16 * (k & 1))) & 0xFFFFu;
+          sum[k] += n;
+          sum_prev[k] += before ? n : 0;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (8 * col + k < a.E) {
+          if (sum[k] != 0) atomicAdd(&all[8 * col + k], sum[k]);
+          if (sum_prev[k] != 0) atomicAdd(&prev[8 * col + k], sum_prev[k]);
+        }
+    }
+  }
+  __syncthreads();
+  // Expert starts: two experts a thread, a block scan.
+  const int e0 = 2 * threadIdx.x;
+  const int n0 = e0 < a.E ? all[e0] : 0, n1 = e0 + 1 < a.E ? all[e0 + 1] : 0;
+  int scan = n0 + n1;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
     if (lane >= d) scan += v;
   }
   if (lane == 31) warp_sum[warp] = scan;
-  for (int e = lane; e < a.E; e += 32) before[warp][e] = 0;
   __syncthreads();
-  int at = scan - all[0] - all[1];
+  int at = scan - n0 - n1;
   for (int w = 0; w < warp; ++w) at += warp_sum[w];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
-    if (e < a.E) {
-      start[e] = at + prev[i];
-      if (blockIdx.x == 0) a.offsets[e] = at;
-    }
-    at += all[i];
-    if (e == a.E - 1 && blockIdx.x == 0) a.offsets[a.E] = at;
-  }
-  const int c0 = blockIdx.x * a.per_cta, c1 = min(a.T, c0 + a.per_cta);
-  const int t0 = min(c1, c0 + warp * a.per_warp), t1 = min(c1, t0 + a.per_warp);
-  // A token's picks are distinct, so its lanes never meet on one counter.
-  for (int t = t0; t < t1; ++t) {
-    if (lane < a.top_k) ++before[warp][a.ids[static_cast<size_t>(t) * a.top_k + lane]];
-    __syncwarp();
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kRtThreads) {
-    int sum = 0;
-    for (int w = 0; w < kRtWarps; ++w) {
-      const int n = before[w][e];
-      before[w][e] = static_cast<uint16_t>(sum);
-      sum += n;
-    }
+  if (e0 < a.E) start[e0] = at + prev[e0];
+  if (e0 + 1 < a.E) start[e0 + 1] = at + n0 + prev[e0 + 1];
+  if (blockIdx.x == 0) {
+    if (e0 < a.E) a.offsets[e0] = at;
+    if (e0 + 1 < a.E) a.offsets[e0 + 1] = at + n0;
+    if (e0 < a.E && e0 + 2 >= a.E) a.offsets[a.E] = at + n0 + n1;
   }
   __syncthreads();
   for (int t = t0; t < t1; ++t) {
     if (lane < a.top_k) {
-      const int route = t * a.top_k + lane;
-      const int e = a.ids[route];
-      const int place = start[e] + before[warp][e]++;
-      a.rows[place] = route;
+      const int r = t * a.top_k + lane;
+      const int e = a.ids[r];  // this thread's own store
+      const int place = start[e] + seen[warp][e]++;
+      a.rows[place] = r;
       a.tokens[place] = t;
     }
     __syncwarp();
@@ -193,12 +253,13 @@ __global__ void __launch_bounds__(kRtThreads) route_place_kernel(const RtArgs a)
 }
 
 static int rt_ctas(int T) {
-  const int n = (T + kRtWarps - 1) / kRtWarps;
-  return n < kRtMaxCtas ? n : kRtMaxCtas;
+  const int n = (T + kRtTokens - 1) / kRtTokens;
+  return n < 1 ? 1 : n < kRtMaxCtas ? n : kRtMaxCtas;
 }
+static int rt_pitch(int E) { return (E + 7) & ~7; }
 
 size_t route_workspace_bytes(int T, int E) {
-  return 256 + ((static_cast<size_t>(rt_ctas(T)) * E * sizeof(uint16_t) + 255) & ~size_t(255));
+  return 256 + ((static_cast<size_t>(rt_ctas(T)) * rt_pitch(E) * sizeof(uint16_t) + 255) & ~size_t(255));
 }
 
 int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale, int32_t* ids,
@@ -212,23 +273,33 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
     if (err != cudaSuccess) return set_last_error(FME_ECUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
     return FME_OK;
   }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_last_error(FME_ECUDA, "cudaGetDevice failed");
+  const int sms = device_sm_count(dev);
+  if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
   RtArgs a = {};
   a.logits = logits;
   a.bias = bias;
   a.logits_f32 = logits_dtype == FME_F32;
+  a.vec = E % 8 == 0;  // rows of logits are then whole 16-byte units
   a.T = T;
   a.E = E;
   a.top_k = top_k;
   a.scale = scale;
-  const int ctas = rt_ctas(T);
+  // All CTAs of a launch meet, so there are no more than SMs.
+  const int ctas = rt_ctas(T) < sms ? rt_ctas(T) : sms;
   a.per_cta = (T + ctas - 1) / ctas;
   a.per_warp = (a.per_cta + kRtWarps - 1) / kRtWarps;
+  a.pitch = rt_pitch(E);
   a.ids = ids;
   a.weights = weights;
   a.offsets = offsets;
   a.rows = rows;
   a.tokens = tokens;
+  a.err = static_cast<uint32_t*>(workspace);
+  a.sync = a.err + 16;
   a.counts = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + 256);
+  a.timeout_ns = wait_timeout_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kRtThreads);
@@ -238,14 +309,8 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t err;
-  if (E <= 64)
-    err = cudaLaunchKernelEx(&cfg, route_pick_kernel<2>, a);
-  else if (E <= 256)
-    err = cudaLaunchKernelEx(&cfg, route_pick_kernel<8>, a);
-  else
-    err = cudaLaunchKernelEx(&cfg, route_pick_kernel<32>, a);
-  if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, route_place_kernel, a);
+  void (*kernel)(RtArgs) = E <= 64 ? route_kernel<2> : E <= 256 ? route_kernel<8> : E <= 512 ? route_kernel<16> : route_kernel<32>;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "route launch: %s", cudaGetErrorString(err));
   return FME_OK;
 }

@@ -420,7 +420,8 @@ int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, lo
  *   top_k). 0 <= T <= 2^20 (0: offsets are zeroed), E in [1, 1024], top_k in
  *   [1, min(E, 32)]. NaN logits give picks that are distinct and in range.
  *   Every pointer 16-byte aligned. The workspace (see
- *   fme_moe_route_workspace) needs no zeroing. Errors: FME_OK, FME_EINVAL,
+ *   fme_moe_route_workspace) must be zeroed before its first use; a
+ *   workspace sized for T serves every smaller T. Errors: FME_OK, FME_EINVAL,
  *   FME_EUNSUPPORTED, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA.
  */
 int fme_moe_route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale,
