@@ -125,15 +125,11 @@ __device__ __forceinline__ float quotient(float h, float s, float inv) {
   const float q = __fmul_rn(h, inv);
   return __fmaf_rn(__fmaf_rn(-q, s, h), inv, q);
 }
-// g / (1 + exp(-g)) with the decode kernel's roundings (expf, a rounded quotient), the reciprocal by a Newton step on
-// the hardware's approximation. Below -80, where the exact value is under 1e-33 and its E4M3 code zero, exp stays at
-// exp(80), so that no infinity meets the Newton step.
+// g / (1 + exp(-g)) with the decode kernel's roundings (expf, a rounded quotient): equal for every float above -80.
+// Below, where the exact value is under 1e-33 and its E4M3 code zero, exp stays at exp(80), in recip_rn's range.
 __device__ __forceinline__ float silu(float g) {
   const float d = __fadd_rn(1.0f, expf(fminf(-g, 80.0f)));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  r = __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
-  return quotient(g, d, r);
+  return quotient(g, d, recip_rn(d));
 }
 // (lo, hi) rounded to BF16, lo in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

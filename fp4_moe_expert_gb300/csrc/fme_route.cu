@@ -8,16 +8,18 @@
 // for its run and counts its routes per expert in shared memory; the CTAs publish their counts, meet once (bounded
 // wait), and each derives the expert starts and its own places from all counts. So every route has its place without
 // an atomic whose order could show.
-// Bound by latency: a pick round is a warp maximum and one lane's search for its next best.
+// Bound by instruction issue on long prompts (a token's keys, and the choice among them) and by latency on short ones.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
 namespace fme {
 
-constexpr int kRtWarps = 16;
-constexpr int kRtThreads = 32 * kRtWarps;
 constexpr int kRtMaxCtas = 152;
 constexpr int kRtTokens = 16;  // least tokens a CTA is given, where there are as many
+constexpr int kRtIds = 64;     // picks of its run that a warp keeps in shared memory; the rest it reads back
+// Warps a CTA: 32 where a lane's experts (J) leave 64 registers enough, else 16.
+template <int J>
+__host__ __device__ constexpr int rt_warps() { return J <= 8 ? 32 : 16; }
 
 struct RtArgs {
   const void* logits;
@@ -37,29 +39,34 @@ struct RtArgs {
   unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ float rt_sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
-__device__ __forceinline__ float rt_logit(const RtArgs& a, size_t i) {
-  return a.logits_f32 ? __ldg(static_cast<const float*>(a.logits) + i)
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[i]);
+__device__ __noinline__ float rt_recip_far(float d) { return __fdiv_rn(1.0f, d); }
+// route_topk's sigmoid, bit for bit.
+__device__ __forceinline__ float rt_sigmoid(float l) {
+  const float d = __fadd_rn(1.0f, expf(-l));
+  return d <= 0x1p125f ? recip_rn(d) : rt_recip_far(d);
+}
+__device__ __forceinline__ float rt_value(const void* from, bool f32, size_t i) {
+  return f32 ? __ldg(static_cast<const float*>(from) + i)
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(from)[i]);
 }
 
-// The logits of experts J * lane .. J * lane + J - 1 of token t (J a multiple of 8: in 16-byte loads where rows allow).
+// Values J * lane .. J * lane + J - 1 of the row of E that starts at element `row` (J a multiple of 8: in 16-byte loads
+// where rows allow).
 template <int J>
-__device__ __forceinline__ void rt_load(const RtArgs& a, int t, int lane, float (&l)[J]) {
-  const size_t row = static_cast<size_t>(t) * a.E;
+__device__ __forceinline__ void rt_load(const RtArgs& a, const void* from, bool f32, size_t row, int lane, float (&l)[J]) {
   const int e0 = J * lane;
   if (J >= 8 && a.vec) {
 #pragma unroll
     for (int j = 0; j < J; j += 8)
       if (e0 + j < a.E) {
-        if (a.logits_f32) {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0 + j);
+        if (f32) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(from) + row + e0 + j);
           const float4 p = __ldg(src), q = __ldg(src + 1);
           l[j] = p.x, l[j + 1] = p.y, l[j + 2] = p.z, l[j + 3] = p.w;
           l[j + 4] = q.x, l[j + 5] = q.y, l[j + 6] = q.z, l[j + 7] = q.w;
         } else {
           const uint4 p =
-              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) + row + e0 + j));
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + row + e0 + j));
           const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -71,49 +78,80 @@ __device__ __forceinline__ void rt_load(const RtArgs& a, int t, int lane, float 
   } else {
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (e0 + j < a.E) l[j] = rt_logit(a, row + e0 + j);
+      if (e0 + j < a.E) l[j] = rt_value(from, f32, row + e0 + j);
   }
 }
 
-// The picks of token t: lane r < top_k gets rank r's expert and weight.
+// Sorts v over the warp, largest in lane 0 (bitonic).
+template <typename V>
+__device__ __forceinline__ V rt_sort(V v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d >= 1; d >>= 1) {
+      const V o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+      const bool keep_larger = ((lane & d) == 0) == ((lane & size) == 0 || size == 32);
+      v = (v > o) == keep_larger ? v : o;
+    }
+  return v;
+}
+
+// The picks of token t: lane r < top_k gets rank r's expert and weight. `cand`: 32 words of this warp's.
+//
+// The top_k-th largest of the 32 lane maxima is at most the top_k-th largest key. The keys from it up are few (about
+// 9 of 256 for 8 picks, 22 of 896 for 16): they move to one a lane and are sorted, key first, lower expert first.
+// Where they are more than 32, the picks are taken one after another instead.
 template <int J>
 __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J], const float (&l)[J], int t, int lane,
-                                        int& my_e, float& my_w) {
+                                        unsigned long long* cand, int& my_e, float& my_w) {
   uint32_t ky[J];
   uint32_t best = 0u;
-  int best_j = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     // At least 1, so that an expert (a NaN key, too) always stands above a lane's empty places.
     ky[j] = J * lane + j < a.E ? max(1u, ordered_key(__fadd_rn(rt_sigmoid(l[j]), bias[j]))) : 0u;
-    if (ky[j] > best) {
-      best = ky[j];
-      best_j = j;
-    }
+    best = max(best, ky[j]);
   }
-  int mine = 0;
-#pragma unroll 1
-  for (int r = 0; r < a.top_k; ++r) {
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    // Lower lanes hold lower experts, and a lane's best is its lowest of equals.
-    const int win = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;
-    const int e = __shfl_sync(0xFFFFFFFFu, J * lane + best_j, win);
-    if (lane == r) mine = e;
-    if (lane == win) {
-      best = 0u;
-      int next = 0;
+  const uint32_t floor_key = max(1u, __shfl_sync(0xFFFFFFFFu, rt_sort(best, lane), a.top_k - 1));
+  int count = 0;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (j == best_j) ky[j] = 0u;
-        if (ky[j] > best) {
-          best = ky[j];
-          next = j;
-        }
-      }
-      best_j = next;
+  for (int j = 0; j < J; ++j) {
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, ky[j] >= floor_key);
+    if (m != 0u) {
+      const int at = count + __popc(m & ((1u << lane) - 1u));
+      if (ky[j] >= floor_key && at < 32)
+        cand[at] = (static_cast<unsigned long long>(ky[j]) << 32) | (0xFFFFFFFFu - (J * lane + j));
+      count += __popc(m);
     }
   }
-  const float s = lane < a.top_k ? rt_sigmoid(rt_logit(a, static_cast<size_t>(t) * a.E + mine)) : 0.0f;
+  __syncwarp();
+  int mine;
+  if (count <= 32) {
+    mine = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(rt_sort(lane < count ? cand[lane] : 0ull, lane)));
+    __syncwarp();
+  } else {
+    mine = 0;
+#pragma unroll 1
+    for (int r = 0; r < a.top_k; ++r) {
+      uint32_t top = 0u;
+      int top_j = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (ky[j] > top) {
+          top = ky[j];
+          top_j = j;
+        }
+      // Lower lanes hold lower experts, and a lane's best is its lowest of equals.
+      const int win = __ffs(__ballot_sync(0xFFFFFFFFu, top == __reduce_max_sync(0xFFFFFFFFu, top))) - 1;
+      const int e = __shfl_sync(0xFFFFFFFFu, J * lane + top_j, win);
+      if (lane == r) mine = e;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (lane == win && j == top_j) ky[j] = 0u;
+    }
+  }
+  const float s =
+      lane < a.top_k ? rt_sigmoid(rt_value(a.logits, a.logits_f32, static_cast<size_t>(t) * a.E + mine)) : 0.0f;
   float total = 0.0f;
   for (int r = 0; r < a.top_k; ++r) total = __fadd_rn(total, __shfl_sync(0xFFFFFFFFu, s, r));
   my_e = mine;
@@ -121,10 +159,15 @@ __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J],
 }
 
 template <int J>
-__global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
-  __shared__ uint16_t seen[kRtWarps][kMaxExperts];  // routes of a warp's run per expert, then its next place
-  __shared__ int all[kMaxExperts], prev[kMaxExperts];  // routes of every CTA, and of those before this one
-  __shared__ int start[kMaxExperts];                   // where this CTA's routes of an expert go
+__global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs a) {
+  constexpr int kRtWarps = rt_warps<J>(), kRtThreads = 32 * kRtWarps;
+  __shared__ uint16_t seen[kRtWarps][32 * J];    // routes of a warp's run per expert, then its next place
+  __shared__ uint16_t picks[kRtWarps][kRtIds];   // the first picks of the run
+  __shared__ union {
+    unsigned long long cand[kRtWarps][32];  // while picking
+    int start[32 * J];                      // then: where this CTA's routes of an expert go
+  } u;
+  __shared__ int all[32 * J], prev[32 * J];      // routes of every CTA, and of those before this one
   __shared__ int warp_sum[kRtWarps];
   __shared__ int gave_up;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = gridDim.x;
@@ -137,20 +180,20 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
   if (t0 < t1) {
     float bias[J], l[J], next[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      bias[j] = J * lane + j < a.E ? __ldg(a.bias + J * lane + j) : 0.0f;
-      l[j] = next[j] = 0.0f;
-    }
-    rt_load<J>(a, t0, lane, l);
+    for (int j = 0; j < J; ++j) bias[j] = l[j] = next[j] = 0.0f;
+    rt_load<J>(a, a.logits, a.logits_f32, static_cast<size_t>(t0) * a.E, lane, l);
+    rt_load<J>(a, a.bias, true, 0, lane, bias);
     __syncwarp();
     for (int t = t0; t < t1; ++t) {
-      if (t + 1 < t1) rt_load<J>(a, t + 1, lane, next);
+      if (t + 1 < t1) rt_load<J>(a, a.logits, a.logits_f32, static_cast<size_t>(t + 1) * a.E, lane, next);
       int e;
       float w;
-      rt_pick<J>(a, bias, l, t, lane, e, w);
+      rt_pick<J>(a, bias, l, t, lane, u.cand[warp], e, w);
       if (lane < a.top_k) {
         a.ids[static_cast<size_t>(t) * a.top_k + lane] = e;
         a.weights[static_cast<size_t>(t) * a.top_k + lane] = w;
+        const int i = (t - t0) * a.top_k + lane;
+        if (i < kRtIds) picks[warp][i] = static_cast<uint16_t>(e);
         ++seen[warp][e];  // a token's picks are distinct: its lanes never meet on one counter
       }
       __syncwarp();
@@ -219,7 +262,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
     }
   }
   __syncthreads();
-  // Expert starts: two experts a thread, a block scan.
+  // Expert starts: two experts a thread (512 threads hold them all), a block scan.
   const int e0 = 2 * threadIdx.x;
   const int n0 = e0 < a.E ? all[e0] : 0, n1 = e0 + 1 < a.E ? all[e0 + 1] : 0;
   int scan = n0 + n1;
@@ -232,8 +275,8 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
   __syncthreads();
   int at = scan - n0 - n1;
   for (int w = 0; w < warp; ++w) at += warp_sum[w];
-  if (e0 < a.E) start[e0] = at + prev[e0];
-  if (e0 + 1 < a.E) start[e0 + 1] = at + n0 + prev[e0 + 1];
+  if (e0 < a.E) u.start[e0] = at + prev[e0];
+  if (e0 + 1 < a.E) u.start[e0 + 1] = at + n0 + prev[e0 + 1];
   if (blockIdx.x == 0) {
     if (e0 < a.E) a.offsets[e0] = at;
     if (e0 + 1 < a.E) a.offsets[e0 + 1] = at + n0;
@@ -243,8 +286,9 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RtArgs a) {
   for (int t = t0; t < t1; ++t) {
     if (lane < a.top_k) {
       const int r = t * a.top_k + lane;
-      const int e = a.ids[r];  // this thread's own store
-      const int place = start[e] + seen[warp][e]++;
+      const int i = (t - t0) * a.top_k + lane;
+      const int e = i < kRtIds ? picks[warp][i] : a.ids[r];  // this lane's own store
+      const int place = u.start[e] + seen[warp][e]++;
       a.rows[place] = r;
       a.tokens[place] = t;
     }
@@ -289,7 +333,8 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   // All CTAs of a launch meet, so there are no more than SMs.
   const int ctas = rt_ctas(T) < sms ? rt_ctas(T) : sms;
   a.per_cta = (T + ctas - 1) / ctas;
-  a.per_warp = (a.per_cta + kRtWarps - 1) / kRtWarps;
+  const int warps = E <= 256 ? rt_warps<8>() : rt_warps<32>();
+  a.per_warp = (a.per_cta + warps - 1) / warps;
   a.pitch = rt_pitch(E);
   a.ids = ids;
   a.weights = weights;
@@ -302,7 +347,7 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   a.timeout_ns = wait_timeout_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kRtThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
