@@ -33,11 +33,12 @@
 namespace fme {
 
 constexpr int kGrThreads = 384;
+constexpr int kGrAccWarps = 8;
 constexpr int kGrGatherThreads = 64;
-// Registers a thread: 384 x 168 at launch, then 8 accumulate warps x 216 and 4 others x 72 (the same sum).
+// Registers a thread: 384 x 168 at launch, then 8 accumulate warps x 216 and 4 others x 72 (the same sum): without the
+// split the accumulators spill (16 experts x 512 rows: gate/up 218 -> 228 us, down 123 -> 138 us).
 constexpr int kGrLaunchRegs = 168, kGrAccRegs = 216, kGrOtherRegs = 72;
 static_assert(2 * kGrAccRegs + kGrOtherRegs == 3 * kGrLaunchRegs, "register split");
-constexpr int kGrAccWarps = 8;
 // Scales travel in groups of up to four K blocks of a tile. The producer fills a group's slot once the MMA of the K block
 // four before its first is done, which waited for the accumulate warps to leave the K block two before that: the
 // groups still read are at most five back.
@@ -71,8 +72,9 @@ struct GrArgs {
 struct GrShared {
   float4 sx[kGrSlots][128];  // activation scales of the rows, four K blocks
   float4 sw[kGrSlots][2];    // weight scales of the two 128-row boxes
-  uint64_t full[kGrStages], empty[kGrStages];
-  uint64_t tfull[2], tempty[2];
+  uint64_t full[kGrStages];  // a stage's operands have landed
+  uint64_t done[kGrStages];  // its MMAs have completed: the stage is free and the accumulator complete
+  uint64_t tempty[2];        // an accumulator buffer has been read
   uint64_t sfull[kGrSlots];
   uint64_t drain;
   uint32_t tmem;
@@ -91,10 +93,18 @@ struct GrTile {
 };
 
 // Tile t: groups in order, within a group the row tiles of one weight tile are
-// neighbours, so CTAs running at the same time share the weights through L2.
-__device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles, int t) {
+// neighbours, so CTAs running at the same time share the weights through L2. `from`:
+// a group not after t's, where the search starts (the last tile's group).
+__device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles, int t, int from) {
   const int x = t / n_tiles;
-  int lo = 0, hi = E;  // tiles[lo] <= x < tiles[hi]
+  int lo = from, hi = E;  // tiles[lo] <= x < tiles[hi]
+  // Usually a step or two on; else halving what is left.
+  for (int i = 0; i < 3 && hi - lo > 1; ++i) {
+    if (S.tiles[lo + 1] <= x)
+      ++lo;
+    else
+      hi = lo + 1;
+  }
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (S.tiles[mid] <= x)
@@ -155,10 +165,9 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   if (tid == 0) {
     for (int s = 0; s < kGrStages; ++s) {
       mbar_init(&S.full[s], 1 + kGrGatherThreads);
-      mbar_init(&S.empty[s], 1);
+      mbar_init(&S.done[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&S.tfull[b], 1);
       mbar_init(&S.tempty[b], kGrAccWarps);
     }
     for (int s = 0; s < kGrSlots; ++s) mbar_init(&S.sfull[s], 32);
@@ -218,10 +227,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   if (warp == 8) {
     // ------------------------------------------------------------ loads
     uint32_t it = 0, group = 0;
+    int from = 0;
     const bool vec = KB % 4 == 0;  // rows of scales are whole 16-byte units
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      const GrTile g = gr_tile(S, a.E, n_tiles, t, from);
+      from = g.e;
       const bool box = a.in_rows == nullptr && g.rows == 128;
       const float* sa[4];
 #pragma unroll
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const uint32_t bytes = (box ? kGrABytes : 0) + (two ? 2 : 1) * kGrBoxBytes;
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages;
-        ok = mbar_wait_spin(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.done[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes;
@@ -290,8 +301,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           const uint64_t ad = desc0 + s * (kGrStageBytes >> 4), bd = ad + (kGrABytes >> 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + 256 * b, ad + 2 * i, bd + 2 * i, f8_idesc(128, 256), i != 0);
-          tc_commit(&S.empty[s]);
-          tc_commit(&S.tfull[b]);
+          tc_commit(&S.done[s]);
         }
         __syncwarp();
       }
@@ -317,9 +327,11 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       mbar_arrive(&S.full[k % kGrStages]);
     };
     uint32_t it = 0;
+    int from = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      const GrTile g = gr_tile(S, a.E, n_tiles, t, from);
+      from = g.e;
       const bool box = a.in_rows == nullptr && g.rows == 128;
       int row[16];
 #pragma unroll
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       for (int j = 0; j < KB; ++j, ++it, src += 128) {
         if (it >= kLag) land(it - kLag);
         const uint32_t s = it % kGrStages;
-        ok = mbar_wait_spin(&S.empty[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.done[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes + dst0;
 #pragma unroll
@@ -359,15 +371,17 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       if (lane == 0) mbar_arrive(&S.tempty[b]);
     };
     uint32_t it = 0, group = 0, slot = 0;
-    int parity = 0;
+    int parity = 0, from = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total; t += gridDim.x, parity ^= 1) {
-      const GrTile g = gr_tile(S, a.E, n_tiles, t);
+      const GrTile g = gr_tile(S, a.E, n_tiles, t, from);
+      from = g.e;
       const bool columns = SWIGLU || 256 * g.n + 128 * half < a.N;
       const bool live = 32 * quad < g.rows && columns;  // this warp has rows (and columns) to hold
       const int p = g.p0 + min(row, g.rows - 1);
       const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
       const bool bad = r < 0 || r >= a.a_rows;
+      const int o = SWIGLU || a.out_rows == nullptr ? p : __ldg(a.out_rows + p);
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
@@ -377,29 +391,23 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           slot = group % kGrSlots;
           ok = ok && mbar_wait_spin(&S.sfull[slot], (group++ / kGrSlots) & 1, a.timeout_ns, abort);
         }
-        ok = ok && mbar_wait_spin(&S.tfull[b], (it >> 1) & 1, a.timeout_ns, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
         const float sx = (&S.sx[slot][row].x)[j & 3];
         const float s0 = __fmul_rn((&S.sw[slot][SWIGLU ? 0 : half].x)[j & 3], sx);
         const float s1 = SWIGLU ? __fmul_rn((&S.sw[slot][1].x)[j & 3], sx) : s0;
+        ok = ok && mbar_wait_spin(&S.done[it % kGrStages], (it / kGrStages) & 1, a.timeout_ns, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         if (live) {
           tc_fence_after();
-          // Sixteen columns ahead: one load is in flight while the other's values are added.
           const uint32_t base = lanes + 256 * b + (SWIGLU ? 64 : 128) * half;
-          float d[2][16];
-          tmem_ld_issue(base, d[0]);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            tmem_ld_join(d[c & 1]);
-            if (c < 7)
-              tmem_ld_issue(base + (SWIGLU && c >= 3 ? 64 : 0) + 16 * (c + 1), d[(c + 1) & 1]);
-            else
-              release(b);
-            const float s = c < 4 ? s0 : s1;
+            float d[16];
+            tmem_ld_issue(base + (SWIGLU && c >= 4 ? 64 : 0) + 16 * c, d);
+            tmem_ld_join(d);
+            if (c == 7) release(b);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              fma2(acc[16 * c + i], acc[16 * c + i + 1], d[c & 1][i], d[c & 1][i + 1], s);
+            for (int i = 0; i < 16; ++i) acc[16 * c + i] = __fmaf_rn(d[i], c < 4 ? s0 : s1, acc[16 * c + i]);
           }
         } else {
           __syncwarp();
@@ -449,7 +457,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       } else {
         if (!ok) break;
         if (row < g.rows && columns) {
-          const int o = a.out_rows != nullptr ? __ldg(a.out_rows + p) : p;
           if (o < 0 || o >= a.out_n) {
             atomicOr(a.err, kErrRoute);
           } else {

@@ -119,14 +119,25 @@ __device__ __forceinline__ bool named_bar_or(int id, int threads, bool pred) {
   return r != 0;
 }
 
-// mbar_wait for waits that are short and many: the timer is first read after 64 tries.
+// One try that may sleep up to `ns` before it gives up: a warp that sleeps leaves the others the issue slots and the
+// shared-memory pipe that polling takes.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait for waits that are many: it sleeps, and reads the timer late.
 __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                const volatile int* abort) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (n % 64 == 0) {
+    if (mbar_try_wait_for(bar, parity, 20000)) return true;
+    if (n % 16 == 0) {
       if (abort != nullptr && *abort) return false;
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
@@ -159,6 +170,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r));
   return r != 0;
 }
+
 // Registers per thread of the calling warpgroup, up (inc) or down (dec); every warp of it executes this.
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -381,13 +393,6 @@ __device__ __forceinline__ void tmem_ld_join(float (&r)[16]) {
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
                  "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
                  "+f"(r[15])::"memory");
-}
-// (a0, a1) += (d0, d1) * (s, s), two FP32 fused multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(float& a0, float& a1, float d0, float d1, float s) {
-  asm("{ .reg .b64 a, d, t; mov.b64 a, {%0, %1}; mov.b64 d, {%2, %3}; mov.b64 t, {%4, %4}; fma.rn.f32x2 a, d, t, a; "
-      "mov.b64 {%0, %1}, a; }"
-      : "+f"(a0), "+f"(a1)
-      : "f"(d0), "f"(d1), "f"(s));
 }
 // Store sixteen 32-bit columns of this thread's TMEM lane (warp-wide, 32x32b shape).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
