@@ -59,6 +59,7 @@ struct GrArgs {
   const int32_t* out_rows;  // null: row p
   int a_rows, R, out_n, K, N, E;
   int up0, gate0;  // first up / gate weight row (swiglu)
+  int tile_n;      // weight rows a tile: 256, or 128 (gemm)
   float limit;
   int ue8m0;
   int wide;  // out is 32-byte aligned: whole sectors a store
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   GrShared& S = *reinterpret_cast<GrShared*>(ring + kGrStages * kGrStageBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int KB = a.K / 128;
-  const int n_tiles = SWIGLU ? a.N / 256 : (a.N + 255) / 256;
+  const int n_tiles = SWIGLU ? a.N / 256 : (a.N + a.tile_n - 1) / a.tile_n;
 
   if (tid == 0) {
     for (int s = 0; s < kGrStages; ++s) {
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     prefetch_tmap(&a.mapa);
     prefetch_tmap(&a.mapw);
   }
+  griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
   // Row tiles before each group: every thread a few groups, then a block scan.
   constexpr int kPer = (kMaxExperts + kGrThreads - 1) / kGrThreads;
@@ -238,10 +240,11 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < 4; ++i) sa[i] = a.sa + static_cast<size_t>(gr_row(a, g, 4 * lane + i)) * KB;
       // Lane i < 2: the scales of weight box i.
-      const int wb = SWIGLU ? (lane == 0 ? a.up0 : a.gate0) / 128 + g.n : min(2 * g.n + lane, a.N / 128 - 1);
+      const int wb =
+          SWIGLU ? (lane == 0 ? a.up0 : a.gate0) / 128 + g.n : min(g.n * (a.tile_n / 128) + lane, a.N / 128 - 1);
       const float* sw = a.sw + (static_cast<size_t>(g.e) * (a.N / 128) + wb) * KB;
-      const int row0 = SWIGLU ? a.up0 + 128 * g.n : 256 * g.n, row1 = SWIGLU ? a.gate0 + 128 * g.n : row0 + 128;
-      const bool two = row1 < a.N;  // the last tile may have one box only
+      const int row0 = SWIGLU ? a.up0 + 128 * g.n : a.tile_n * g.n, row1 = SWIGLU ? a.gate0 + 128 * g.n : row0 + 128;
+      const bool two = SWIGLU || (a.tile_n == 256 && row1 < a.N);  // the last tile may have one box only
       const uint32_t bytes = (box ? kGrABytes : 0) + (two ? 2 : 1) * kGrBoxBytes;
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages;
@@ -289,6 +292,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     uint32_t it = 0;
     bool ok = true;
     const uint64_t desc0 = sw128_desc(smem_u32(ring));
+    const uint32_t idesc = SWIGLU || a.tile_n == 256 ? f8_idesc(128, 256) : f8_idesc(128, 128);
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages, b = it & 1;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           // The start address is the descriptor's low field, in units of 16 bytes.
           const uint64_t ad = desc0 + s * (kGrStageBytes >> 4), bd = ad + (kGrABytes >> 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + 256 * b, ad + 2 * i, bd + 2 * i, f8_idesc(128, 256), i != 0);
+          for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + 256 * b, ad + 2 * i, bd + 2 * i, idesc, i != 0);
           tc_commit(&S.done[s]);
         }
         __syncwarp();
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     for (int t = blockIdx.x; t < total; t += gridDim.x, parity ^= 1) {
       const GrTile g = gr_tile(S, a.E, n_tiles, t, from);
       from = g.e;
-      const bool columns = SWIGLU || 256 * g.n + 128 * half < a.N;
+      const bool columns = SWIGLU || (128 * half < a.tile_n && a.tile_n * g.n + 128 * half < a.N);
       const bool live = 32 * quad < g.rows && columns;  // this warp has rows (and columns) to hold
       const int p = g.p0 + min(row, g.rows - 1);
       const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           if (o < 0 || o >= a.out_n) {
             atomicOr(a.err, kErrRoute);
           } else {
-            __nv_bfloat16* dst = a.out + static_cast<size_t>(o) * a.N + 256 * g.n + 128 * half;
+            __nv_bfloat16* dst = a.out + static_cast<size_t>(o) * a.N + a.tile_n * g.n + 128 * half;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t w[8];
@@ -556,9 +560,14 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   a.err = static_cast<uint32_t*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   const bool swiglu = g.q != nullptr;
-  const long long n_tiles = swiglu ? g.N / 256 : (g.N + 255) / 256;
-  // No more CTAs than the most tiles these sizes can make (a group's last row tile may be part empty).
-  const long long most = (static_cast<long long>(g.R) / 128 + (g.R < g.E ? g.R : g.E)) * n_tiles;
+  // At most so many row tiles (a group's last may be part empty).
+  const long long row_tiles = static_cast<long long>(g.R) / 128 + (g.R < g.E ? g.R : g.E);
+  auto tiles = [&](int tile_n) { return row_tiles * ((g.N + tile_n - 1) / tile_n); };
+  auto waves = [&](int tile_n) { return (tiles(tile_n) + sms - 1) / sms * tile_n; };
+  // Half as wide gemm tiles where they fill the last wave better (one token of the DeepSeek-V3 shape: 224 tiles are
+  // two waves of 256 columns, 448 three of 128). Wide tiles read the activations once for twice the columns.
+  a.tile_n = !swiglu && 10 * waves(128) < 9 * waves(256) ? 128 : 256;
+  const long long most = tiles(a.tile_n);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
   cfg.blockDim = dim3(kGrThreads);

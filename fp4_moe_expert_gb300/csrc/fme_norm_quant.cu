@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(SMALL ? 32 * kNqSmallRows : 32 * kNqRowWarps) 
   const int t = SMALL ? blockIdx.x * kNqSmallRows + warp : blockIdx.x;
   const int rt = SMALL ? lane : threadIdx.x, width = SMALL ? 32 : blockDim.x;  // thread of the row, threads a row
   const int chunks = t < a.T ? a.H / 8 : 0;
+  griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
   const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.ldx);
   uint4 z[kNqChunks];

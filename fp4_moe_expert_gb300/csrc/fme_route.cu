@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
   for (int e = lane; e < a.E; e += 32) seen[warp][e] = 0;
   for (int e = threadIdx.x; e < a.E; e += kRtThreads) all[e] = prev[e] = 0;
   if (threadIdx.x == 0) gave_up = 0;
+  griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
   const int c0 = min(a.T, static_cast<int>(blockIdx.x) * a.per_cta), c1 = min(a.T, c0 + a.per_cta);
   const int t0 = min(c1, c0 + warp * a.per_warp), t1 = min(c1, t0 + a.per_warp);
