@@ -268,6 +268,40 @@ def test_grouped_swiglu(fme, counts, seed, H, I, limit, ue8m0, gate_first):
     _check_codes(q, np.repeat(s, 128, axis=1), h, dh + 4 * U * np.abs(h))
 
 
+def test_grouped_gemm_wide_tiles(fme):
+    """Enough tiles for 256 output columns each, the last of them half a tile."""
+    K, N = 128, 2176
+    counts = [4100, 0, 1, 2500, 3399]
+    a, sa, w, sw, off, _ = _grouped_inputs(counts, K, N, 10000, 77, False)
+    y, size = prompt.grouped_product(a, sa, w, sw, off)
+    got = _np(fme.moe_grouped_gemm_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off)))
+    assert np.all(np.abs(got - y) <= (K // 128 + 8) * 2 * U * size + np.abs(y) * 2.0 ** -8 * 1.001)
+
+
+def test_grouped_outputs_at_any_16_bytes(fme):
+    a, sa, w, sw, off, _ = _grouped_inputs([70, 60], 256, 384, 130, 78, False)
+    args = (_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off))
+    ref = fme.moe_grouped_gemm_fp8(*args)
+    buf = torch.zeros(130 * 384 + 8, dtype=torch.bfloat16, device=DEV)
+    out = buf[8:].view(130, 384)  # 16 bytes past an allocation's start
+    assert out.data_ptr() % 32 == 16
+    fme.moe_grouped_gemm_fp8(*args, out=out)
+    assert torch.equal(out, ref) and not buf[:8].any()
+
+
+def test_grouped_many_groups(fme):
+    """1024 groups, most of them empty, K blocks that are no multiple of four."""
+    E, K, N = 1024, 384, 128
+    rng = np.random.default_rng(79)
+    counts = np.zeros(E, int)
+    counts[rng.choice(E, 40, replace=False)] = rng.integers(1, 140, size=40)
+    counts[-1] = 5
+    a, sa, w, sw, off, idx = _grouped_inputs(counts, K, N, 60, 80, True)
+    y, size = prompt.grouped_product(a, sa, w, sw, off, idx)
+    got = _np(fme.moe_grouped_gemm_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off), in_rows=_dev(idx)))
+    assert np.all(np.abs(got - y) <= (K // 128 + 8) * 2 * U * size + np.abs(y) * 2.0 ** -8 * 1.001)
+
+
 def test_grouped_offsets_rows_and_errors(fme):
     """Places outside every group stay as they are; offsets out of range are clamped; a bad index gives zeros or is
     skipped, and is reported; NaN codes stay in their row."""
@@ -379,3 +413,41 @@ def test_prompt_operators_in_a_graph(fme):
         torch.cuda.synchronize()
         assert torch.equal(y, step())
     assert [w.error() for w in ws] == [0, 0, 0]
+
+
+def test_streams_have_workspaces_of_their_own(fme):
+    """Calls of two streams that overlap share nothing the binding keeps."""
+    lg = [torch.randn(3000, 256, device=DEV) for _ in range(2)]
+    bias = torch.zeros(256, device=DEV)
+    ref = [fme.moe_route(v, bias, 8) for v in lg]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in lg]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fme.moe_route(lg[i], bias, 8))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(r, ref[i]))
+
+
+def test_prompt_layer_example(fme):
+    """The example's layer against the decode layer. They quantise norms that are one BF16 rounding apart (2^-9 of a
+    value and of a block's scale): about one E4M3 code in fifty differs, a percent of the tokens' norm; the hidden
+    values, 1.6 percent apart, differ in a code in six, which makes 3 to 4 percent of an output (an E4M3 rounding
+    alone is 2.6). Unrelated outputs are more than 100 apart."""
+    import importlib.util
+    import os
+    import sys
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "prompt_layer.py")
+    spec = importlib.util.spec_from_file_location("prompt_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    argv, sys.argv = sys.argv, [path, "--tokens", "333"]
+    try:
+        assert mod.main() < 0.05
+    finally:
+        sys.argv = argv
