@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         ok = mbar_wait_spin2(&S.full[s], (it / kGrStages) & 1, &S.tempty[b], ((it >> 1) & 1) ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
+        // The gather's copies, complete by their arrivals on the stage's barrier, before the MMA's reads. (A fence in the
+        // gather warps would hold each K block's copies up for the last one's: gate/up 218 us instead of FENCE.)
+        fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
           // The start address is the descriptor's low field, in units of 16 bytes.
@@ -329,13 +332,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     // Eight threads copy a row's 128 bytes, swizzled as the MMA's descriptor says.
     const int gt = tid - 320, chunk = gt & 7, r0 = gt >> 3;
     const uint32_t dst0 = r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
-    // K block k's copies are waited for, and shown to the MMA, kLag K blocks later.
-    constexpr uint32_t kLag = 2;
-    auto land = [&](uint32_t k) {
-      cp_async_wait<kLag - 1>();
-      fence_proxy_async_smem();
-      mbar_arrive(&S.full[k % kGrStages]);
-    };
     uint32_t it = 0;
     int from = 0;
     bool ok = true;
@@ -349,24 +345,25 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const int n = box ? 0 : (g.rows - r0 + 7) / 8;  // rows this thread copies
       const uint8_t* src = a.a + 16 * chunk;
       for (int j = 0; j < KB; ++j, ++it, src += 128) {
-        if (it >= kLag) land(it - kLag);
         const uint32_t s = it % kGrStages;
         ok = mbar_wait_spin(&S.done[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes + dst0;
+        if (n == 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
-        cp_async_commit();
+          for (int i = 0; i < 16; ++i) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < n) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+        }
+        cp_async_arrive(&S.full[s]);
       }
     }
-    cp_async_wait_all();
-    fence_proxy_async_smem();
-    if (ok) {
-      for (uint32_t k = it > kLag ? it - kLag : 0; k < it; ++k) mbar_arrive(&S.full[k % kGrStages]);
-    } else {
+    if (!ok) {
       atomicOr(a.err, kErrRingWait);
       S.abort = 1;
+      cp_async_wait_all();
     }
     __syncwarp();
   } else {
@@ -432,12 +429,14 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       if (SWIGLU) {
         // acc[0..63] up, acc[64..127] gate of hidden values 64 * half .. + 63.
         float amax = 0.0f;
+        if (live) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const float up = fminf(fmaxf(acc[c], -a.limit), a.limit);
-          const float gate = fminf(acc[64 + c], a.limit);
-          acc[c] = __fmul_rn(silu(gate), up);
-          amax = fmaxf(amax, fabsf(acc[c]));
+          for (int c = 0; c < 64; ++c) {
+            const float up = fminf(fmaxf(acc[c], -a.limit), a.limit);
+            const float gate = fminf(acc[64 + c], a.limit);
+            acc[c] = __fmul_rn(silu(gate), up);
+            amax = fmaxf(amax, fabsf(acc[c]));
+          }
         }
         S.amax[parity][half][row] = amax;
         // Uniform over the eight warps, so none is left waiting at the next tile's barrier.
