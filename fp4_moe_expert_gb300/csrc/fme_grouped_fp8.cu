@@ -16,7 +16,7 @@
 // the MMA, 10-11 copy activation rows by index.
 // * Loads: per 128-value K block two 128-row boxes of weights by TMA, and the tile's
 //   rows: a full tile of consecutive rows as one box, others row by row with cp.async
-//   (only the rows the group has). TMA's own row gather (tile::gather4) measured
+//   (only the rows the group has; two warps, whose pace tells: predicates on a full tile cost 3 %). TMA's own row gather (tile::gather4) measured
 //   90 clocks for four rows, 2900 a tile and K block against 512 of MMA work.
 // * The scales are FP32 and not powers of two, so the MMA cannot apply them: each
 //   K block is one 128 x 256 accumulation in tensor memory (two buffers), and the
@@ -28,7 +28,7 @@
 // What bounds it: with few rows a group, DRAM (gate/up of the DeepSeek-V3 shape: 8 experts, one row each, 43 us,
 // 5.5 TB/s; 256 experts, 6 rows each, 928 us, 8.0 TB/s). With many, the accumulate warps, about 735 clocks of
 // waits, tensor-memory loads and multiply-adds a K block alone and 950 beside the loads, against 512 of MMA (16 experts x
-// 512 rows: gate/up 218 us, 2200 TFLOP/s; down 121 us, 1990 TFLOP/s), and under sustained load the power limit.
+// 512 rows: gate/up 205 us, 2350 TFLOP/s; down 120 us, 2000 TFLOP/s), and under sustained load the power limit.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         // The gather's copies, complete by their arrivals on the stage's barrier, before the MMA's reads. (A fence in the
-        // gather warps would hold each K block's copies up for the last one's: gate/up 218 us instead of FENCE.)
+        // gather warps would hold each K block's copies up for the last one's: gate/up 217 us instead of 211.)
         fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
