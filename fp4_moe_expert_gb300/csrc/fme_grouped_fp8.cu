@@ -344,20 +344,43 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       for (int i = 0; i < 16; ++i) row[i] = gr_row(a, g, r0 + 8 * i);
       const int n = box ? 0 : (g.rows - r0 + 7) / 8;  // rows this thread copies
       const uint8_t* src = a.a + 16 * chunk;
-      for (int j = 0; j < KB; ++j, ++it, src += 128) {
-        const uint32_t s = it % kGrStages;
-        ok = mbar_wait_spin(&S.done[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+      for (int j = 0; j < KB;) {
+        // Two K blocks a turn: one wait and one address for both.
+        const bool two = j + 1 < KB;
+        const uint32_t s0 = it % kGrStages, s1 = (it + 1) % kGrStages, last = it + (two ? 1 : 0);
+        ok = mbar_wait_spin(&S.done[last % kGrStages], ((last / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         if (!ok) break;
-        uint8_t* st = ring + s * kGrStageBytes + dst0;
-        if (n == 16) {
+        uint8_t* st0 = ring + s0 * kGrStageBytes + dst0;
+        uint8_t* st1 = ring + s1 * kGrStageBytes + dst0;
+        if (two) {
+          if (n == 16) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+            for (int i = 0; i < 16; ++i) {
+              const uint8_t* p = src + static_cast<size_t>(row[i]) * a.K;
+              cp_async_16(st0 + 1024 * i, p);
+              cp_async_16(st1 + 1024 * i, p + 128);
+            }
+            cp_async_arrive(&S.full[s0]);
+            cp_async_arrive(&S.full[s1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < n) {
+                const uint8_t* p = src + static_cast<size_t>(row[i]) * a.K;
+                cp_async_16(st0 + 1024 * i, p);
+                cp_async_16(st1 + 1024 * i, p + 128);
+              }
+            cp_async_arrive(&S.full[s0]);
+            cp_async_arrive(&S.full[s1]);
+          }
+          j += 2, it += 2, src += 256;
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (i < n) cp_async_16(st + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+            if (i < n) cp_async_16(st0 + 1024 * i, src + static_cast<size_t>(row[i]) * a.K);
+          cp_async_arrive(&S.full[s0]);
+          ++j, ++it, src += 128;
         }
-        cp_async_arrive(&S.full[s]);
       }
     }
     if (!ok) {
