@@ -278,6 +278,39 @@ def test_grouped_gemm_wide_tiles(fme):
     assert np.all(np.abs(got - y) <= (K // 128 + 8) * 2 * U * size + np.abs(y) * 2.0 ** -8 * 1.001)
 
 
+def test_grouped_long_launches(fme):
+    """Enough tiles for CTAs in pairs: odd and even counts of row tiles, an odd count of weight tiles, the last of them
+    half. The rows come from 50, so every expected row is one of 50 an expert."""
+    counts = [7001, 0, 12999, 64]
+    E, K, N, I, rows = len(counts), 128, 4224, 2048, 50
+    off = np.cumsum([0] + counts).astype(np.int32)
+    idx = np.random.default_rng(81).integers(0, rows, size=off[-1]).astype(np.int32)
+    which = np.repeat(np.arange(E), counts) * rows + idx
+    every = np.arange(E + 1, dtype=np.int32) * rows
+    a, sa, w, sw, _, _ = _grouped_inputs([1] * E, K, N, rows, 82, False)
+    y, size = prompt.grouped_product(a, sa, w, sw, every, np.tile(np.arange(rows), E))
+    got = _np(fme.moe_grouped_gemm_fp8(_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off), in_rows=_dev(idx)))
+    tol = (K // 128 + 8) * 2 * U * size + np.abs(y) * 2.0 ** -8 * 1.001
+    first = np.array([np.flatnonzero(which == k)[0] if (which == k).any() else -1 for k in range(E * rows)])
+    for k in np.flatnonzero(first >= 0):
+        assert np.all(np.abs(got[first[k]] - y[k]) <= tol[k])
+    assert np.array_equal(got, got[first[which]])  # equal rows give equal rows, wherever their tile ran
+
+    w13, s13 = w[:, :2 * I], sw[:, :2 * I // 128]
+    q, s = fme.moe_grouped_swiglu_fp8(_dev(a), _dev(sa), _dev(w13), _dev(s13), _dev(off), in_rows=_dev(idx), limit=7.0)
+    q, s = _np(q), _np(s).astype(np.float64)
+    up, gate, su, sg = y[:, :I], y[:, I:2 * I], size[:, :I], size[:, I:2 * I]
+    h = clamped_swiglu(gate, up, 7.0)
+    du, dg = ((K // 128 + 8) * 2 * U * v for v in (su, sg))
+    g, u = np.minimum(gate, 7.0), np.clip(up, -7.0, 7.0)
+    dh = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + 16 * U * np.abs(h)
+    for k in np.flatnonzero(first >= 0):
+        base = np.maximum(np.abs(h[k]).reshape(-1, 128).max(-1), 1e-10) / 448
+        assert np.all(np.abs(s[first[k]] - base) <= dh[k].reshape(-1, 128).max(-1) / 448 + 4 * U * base)
+        _check_codes(q[first[k]], np.repeat(s[first[k]], 128), h[k], dh[k] + 4 * U * np.abs(h[k]))
+    assert np.array_equal(q, q[first[which]]) and np.array_equal(s, s[first[which]])
+
+
 def test_grouped_outputs_at_any_16_bytes(fme):
     a, sa, w, sw, off, _ = _grouped_inputs([70, 60], 256, 384, 130, 78, False)
     args = (_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off))
