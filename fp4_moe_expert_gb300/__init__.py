@@ -365,13 +365,16 @@ def ue8m0_unpack(packed, n, k, check=True):
 
 
 def _stream_workspace(nbytes, device, workspace):
-    """The caller's workspace, or one kept per device, current stream and size."""
+    """The caller's workspace, or one kept per device, current stream and size. During a graph capture a new one is the
+    graph's own: zeroed in every replay, and not kept for calls outside it."""
     if workspace is not None:
         return _workspace(nbytes, device, workspace)
     key = (device.index, _stream(device), nbytes)
     ws = _ws_cache.get(key)
     if ws is None:
-        ws = _ws_cache[key] = Workspace(nbytes, device)
+        ws = Workspace(nbytes, device)
+        if not torch.cuda.is_current_stream_capturing():
+            _ws_cache[key] = ws
     return ws
 
 
@@ -538,10 +541,12 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
     moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
 
     xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
-    weights these are. Returns (y [T, H] BF16, ids, weights)."""
+    weights these are. Returns (y [T, H] BF16, ids, weights); no tokens give empty ones."""
     ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale)
     hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0)
     out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows)
+    if xq.shape[0] == 0:
+        return out, ids, weights
     return moe_finalize(out, weights, shared_out), ids, weights
 
 

@@ -484,3 +484,25 @@ def test_prompt_layer_example(fme):
         assert mod.main() < 0.05
     finally:
         sys.argv = argv
+
+
+def test_prompt_layer_without_tokens_and_captured_without_workspaces(fme):
+    cfg, T = W.RAGGED, 40
+    weights = _layer(cfg, 41)
+    routed = (cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0)
+    q = torch.randint(0, 0x7F, (T, cfg.H), dtype=torch.uint8, device=DEV)
+    s = torch.rand(T, cfg.H // 128, device=DEV) * 2.0 ** -8
+    logits, bias = torch.randn(T, cfg.E, device=DEV), torch.zeros(cfg.E, device=DEV)
+    y, ids, _ = fme.moe_prompt_fp8(q[:0], s[:0], logits[:0], bias, *weights, *routed)
+    assert y.shape == (0, cfg.H) and y.dtype == torch.bfloat16 and ids.shape == (0, cfg.top_k)
+    torch.cuda.synchronize()
+    kept = dict(fme._ws_cache)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, _, _ = fme.moe_prompt_fp8(q, s, logits, bias, *weights, *routed)
+    assert set(fme._ws_cache) == set(kept)  # nothing of the graph's memory is kept for other calls
+    for _ in range(3):
+        logits.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, fme.moe_prompt_fp8(q, s, logits, bias, *weights, *routed)[0])
