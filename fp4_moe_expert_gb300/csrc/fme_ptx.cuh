@@ -145,15 +145,6 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, u
     }
   }
 }
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
 // Both barriers' waits at once, so that their latencies overlap.
 __device__ __forceinline__ bool mbar_wait_spin2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
                                                 uint64_t limit_ns, const volatile int* abort) {
