@@ -9,7 +9,7 @@
 // wait), and each derives the expert starts and its own places from all counts. So every route has its place without
 // an atomic whose order could show.
 // Bound by instruction issue on long prompts (a token's keys, and the choice among them: 16384 tokens of 256 experts
-// 22 us) and by latency on short ones (one token 4.5 us, 1533 tokens of 896 experts 21 us).
+// 22 us) and by latency on short ones (one token 4.5 us, 1533 tokens of 896 experts 21 us; 2 us more outside a graph).
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
@@ -351,11 +351,15 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // CTAs that meet run all or none: beside another stream's kernel that waits on its own CTAs, each could otherwise hold
+  // SMs that the other needs. (16384 tokens: 24.6 us instead of 22.0 in a stream, 21.9 either way in a graph.)
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   void (*kernel)(RtArgs) = E <= 64 ? route_kernel<2> : E <= 256 ? route_kernel<8> : E <= 512 ? route_kernel<16> : route_kernel<32>;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "route launch: %s", cudaGetErrorString(err));

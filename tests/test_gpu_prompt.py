@@ -204,6 +204,29 @@ def test_route_of_bad_logits_and_of_no_tokens(fme):
     assert ids.shape == (0, k) and rows.numel() == 0 and not off.any()
 
 
+def test_route_beside_other_streams_of_other_priorities(fme):
+    """Launches whose CTAs meet, beside each other and beside work that holds SMs for a while: all meet."""
+    T, E, k = 3000, 64, 4
+    lg = [torch.randn(T, E, device=DEV) for _ in range(2)]
+    bias = torch.zeros(E, device=DEV)
+    x, gamma = torch.randn(8192, 4096, device=DEV).bfloat16(), torch.ones(4096, device=DEV).bfloat16()
+    want = [fme.moe_route(t, bias, k) for t in lg]
+    ws = [fme.Workspace(fme.moe_route_workspace(T, E, k), DEV) for _ in lg]
+    low, high, busy = torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        with torch.cuda.stream(busy):
+            fme.add_rmsnorm_fp8(x, gamma)
+        for i, s in enumerate((low, high)):
+            with torch.cuda.stream(s):
+                got[i].append(fme.moe_route(lg[i], bias, k, workspace=ws[i]))
+    torch.cuda.synchronize()
+    assert [w.error() for w in ws] == [0, 0]
+    for ref, runs in zip(want, got):
+        assert all(torch.equal(a, b) for run in runs for a, b in zip(run, ref))
+
+
 # --------------------------------------------------------------------------- grouped products
 def _grouped_inputs(counts, H, N, a_rows, seed, gather, ue8m0=False):
     rng = np.random.default_rng(seed)
