@@ -18,8 +18,6 @@
 //   rows: a full tile of consecutive rows as one box, others row by row with cp.async
 //   (only the rows the group has; two warps, whose pace tells: predicates on a full tile cost 3 %). TMA's own row gather (tile::gather4) measured
 //   90 clocks for four rows, 2900 a tile and K block against 512 of MMA work.
-//   PAIR: in long launches two CTAs of a cluster take neighbouring row tiles of one weight tile; each loads one of
-//   its two boxes for both (TMA multicast), which halves what the weights take of the L2's bandwidth and the power.
 // * The scales are FP32 and not powers of two, so the MMA cannot apply them: each
 //   K block is one 128 x 256 accumulation in tensor memory (two buffers), and the
 //   accumulate warps add D * (sw * sa) into 128 registers a thread. A row is a
@@ -57,13 +55,6 @@ constexpr int kGrBoxBytes = 128 * 128;  // 128 weight rows
 constexpr int kGrStages = 4;
 constexpr int kGrStageBytes = kGrABytes + 2 * kGrBoxBytes;
 
-// Two CTAs of a cluster share their weight tiles (PAIR) from this many rows a group on average, in launches of at least
-// this many waves of tiles. 256 experts of the DeepSeek-V3 shape under sustained load, alone / in pairs: 128 rows an
-// expert 1550 / 1527 us (gate/up), 850 / 825 (down); 256 rows 2360 / 2307, 1370 / 1280; 512 rows 3945 / 3845. With
-// 64 rows they are level, and in short launches (16 experts x 192 rows) pairs are slower: 63.5 / 66.5 us (down).
-constexpr int kGrPairRows = 96;
-constexpr int kGrPairWaves = 16;
-
 struct GrArgs {
   CUtensorMap mapa;  // a as [a_rows, K bytes], box 128 rows x 128 bytes (full tiles of consecutive rows)
   CUtensorMap mapw;  // weights as [E * N, K bytes], box 128 rows x 128 bytes
@@ -91,7 +82,6 @@ struct GrShared {
   float4 sw[kGrSlots][2];    // weight scales of the two 128-row boxes
   uint64_t full[kGrStages];  // a stage's operands have landed
   uint64_t done[kGrStages];  // its MMAs have completed: the stage is free and the accumulator complete
-  uint64_t free[kGrStages];  // PAIR: they have in both CTAs (each one's loads write the other's stage)
   uint64_t tempty[2];        // an accumulator buffer has been read
   uint64_t sfull[kGrSlots];
   uint64_t drain;
@@ -107,22 +97,13 @@ constexpr size_t kGrSmemBytes = static_cast<size_t>(kGrStages) * kGrStageBytes +
 static_assert(kGrSmemBytes <= 232448, "shared memory per CTA");
 
 struct GrTile {
-  int e, n, p0, rows;  // expert, weight tile, first row and row count (PAIR: 0 where there is no second weight tile)
-  bool shared;         // PAIR: the other CTA holds a neighbouring row tile of the same weight tile
+  int e, n, p0, rows;  // expert, weight tile, first row and row count
 };
-
-// Tiles of a group of mt row tiles: one per weight tile, or (PAIR) one per two CTAs:
-// two row tiles of one weight tile, and for an odd last row tile two weight tiles.
-template <bool PAIR>
-__device__ __forceinline__ int gr_count(int mt, int n_tiles) {
-  return PAIR ? (mt >> 1) * n_tiles + (mt & 1) * ((n_tiles + 1) >> 1) : mt * n_tiles;
-}
 
 // Tile t: groups in order, within a group the row tiles of one weight tile are
 // neighbours, so CTAs running at the same time share the weights through L2. `from`:
 // a group not after t's, where the search starts (the last tile's group).
-template <bool PAIR>
-__device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles, int t, int from, int rank) {
+__device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int t, int from) {
   int lo = from, hi = E;  // tiles[lo] <= t < tiles[hi]
   // Usually a step or two on; else halving what is left.
   for (int i = 0; i < 3 && hi - lo > 1; ++i) {
@@ -139,32 +120,18 @@ __device__ __forceinline__ GrTile gr_tile(const GrShared& S, int E, int n_tiles,
       hi = mid;
   }
   const int mt = (S.off[lo + 1] - S.off[lo] + 127) / 128;
-  const int per = PAIR ? mt >> 1 : mt;  // (pairs of) row tiles a weight tile
   const int local = t - S.tiles[lo];
   GrTile g;
   g.e = lo;
-  g.shared = local < per * n_tiles;
-  int m;
-  if (g.shared) {
-    g.n = local / per;
-    m = local - g.n * per;
-    if (PAIR) m = 2 * m + rank;
-  } else {
-    g.n = 2 * (local - per * n_tiles) + rank;
-    m = mt - 1;
-  }
-  g.p0 = S.off[lo] + 128 * m;
+  g.n = local / mt;
+  g.p0 = S.off[lo] + 128 * (local - g.n * mt);
   g.rows = min(128, S.off[lo + 1] - g.p0);
-  if (PAIR && g.n >= n_tiles) {
-    g.n = n_tiles - 1;
-    g.rows = 0;
-  }
   return g;
 }
 
 // Row of a that place i of the tile reads (past its end: its last row's; a bad index: row 0, the result is dropped).
 __device__ __forceinline__ int gr_row(const GrArgs& a, const GrTile& g, int i) {
-  const int p = g.p0 + max(0, min(i, g.rows - 1));
+  const int p = g.p0 + min(i, g.rows - 1);
   const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
   return r >= 0 && r < a.a_rows ? r : 0;
 }
@@ -193,7 +160,7 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-template <bool SWIGLU, bool PAIR>
+template <bool SWIGLU>
 __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid_constant__ GrArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -206,7 +173,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     for (int s = 0; s < kGrStages; ++s) {
       mbar_init(&S.full[s], 1 + kGrGatherThreads);
       mbar_init(&S.done[s], 1);
-      mbar_init(&S.free[s], 2);
     }
     for (int b = 0; b < 2; ++b) mbar_init(&S.tempty[b], kGrAccWarps);
     for (int s = 0; s < kGrSlots; ++s) mbar_init(&S.sfull[s], 32);
@@ -226,8 +192,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   griddep_wait();
   // Tiles before each group: every thread a few groups, then a block scan.
   constexpr int kPer = (kMaxExperts + kGrThreads - 1) / kGrThreads;
-  const int rank = PAIR ? cluster_rank() : 0;
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int first = blockIdx.x, step = gridDim.x;
   int own[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -237,7 +202,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const int lo = max(0, min(a.R, __ldg(a.offsets + e)));
       const int hi = max(lo, min(a.R, __ldg(a.offsets + e + 1)));
       S.off[e] = lo;
-      own[i] = gr_count<PAIR>((hi - lo + 127) / 128, n_tiles);
+      own[i] = (hi - lo + 127) / 128 * n_tiles;
       if (e == a.E - 1) S.off[a.E] = hi;
     }
     sum += own[i];
@@ -261,11 +226,9 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     before += own[i];
   }
   __syncthreads();
-  if (PAIR) cluster_sync();  // both CTAs' mbarriers stand before either signals the other's
   const int total = S.tiles[a.E];
   const uint32_t tmem = S.tmem;
   const volatile int* abort = &S.abort;
-  uint64_t* stage_free = PAIR ? S.free : S.done;
   if (warp >= kGrAccWarps) reg_dec<kGrOtherRegs>();
 
   if (warp == 8) {
@@ -275,7 +238,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     const bool vec = KB % 4 == 0;  // rows of scales are whole 16-byte units
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      const GrTile g = gr_tile<PAIR>(S, a.E, n_tiles, t, from, rank);
+      const GrTile g = gr_tile(S, a.E, t, from);
       from = g.e;
       const bool box = a.in_rows == nullptr && g.rows == 128;
       const float* sa[4];
@@ -287,25 +250,17 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
       const float* sw = a.sw + (static_cast<size_t>(g.e) * (a.N / 128) + wb) * KB;
       const int row0 = SWIGLU ? a.up0 + 128 * g.n : a.tile_n * g.n, row1 = SWIGLU ? a.gate0 + 128 * g.n : row0 + 128;
       const bool two = SWIGLU || (a.tile_n == 256 && row1 < a.N);  // the last tile may have one box only
-      const bool idle = PAIR && g.rows == 0;
-      const uint32_t bytes = (box ? kGrABytes : 0) + (idle ? 0 : two ? 2 : 1) * kGrBoxBytes;
+      const uint32_t bytes = (box ? kGrABytes : 0) + (two ? 2 : 1) * kGrBoxBytes;
       for (int j = 0; j < KB; ++j, ++it) {
         const uint32_t s = it % kGrStages;
-        ok = mbar_wait_spin(&stage_free[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.done[s], ((it / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         uint8_t* st = ring + s * kGrStageBytes;
         if (elect_one()) {
           mbar_arrive_expect_tx(&S.full[s], bytes);
-          if (PAIR && g.shared) {
-            // Each CTA loads one of the two boxes for both.
-            if (rank == 0) tma_load_2d_pair(st + kGrABytes, &a.mapw, 128 * j, g.e * a.N + row0, &S.full[s]);
-            if (rank == 1 && two)
-              tma_load_2d_pair(st + kGrABytes + kGrBoxBytes, &a.mapw, 128 * j, g.e * a.N + row1, &S.full[s]);
-          } else if (!idle) {
-            tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, g.e * a.N + row0, &S.full[s]);
-            if (two) tma_load_2d(st + kGrABytes + kGrBoxBytes, &a.mapw, 128 * j, g.e * a.N + row1, &S.full[s]);
-          }
+          tma_load_2d(st + kGrABytes, &a.mapw, 128 * j, g.e * a.N + row0, &S.full[s]);
+          if (two) tma_load_2d(st + kGrABytes + kGrBoxBytes, &a.mapw, 128 * j, g.e * a.N + row1, &S.full[s]);
           if (box) tma_load_2d(st, &a.mapa, 128 * j, g.p0, &S.full[s]);
         }
         __syncwarp();
@@ -360,7 +315,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + 256 * b, ad + 2 * i, bd + 2 * i, idesc, i != 0);
           tc_commit(&S.done[s]);
-          if (PAIR) tc_commit_pair(&S.free[s]);
         }
         __syncwarp();
       }
@@ -382,7 +336,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     int from = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      const GrTile g = gr_tile<PAIR>(S, a.E, n_tiles, t, from, rank);
+      const GrTile g = gr_tile(S, a.E, t, from);
       from = g.e;
       const bool box = a.in_rows == nullptr && g.rows == 128;
       int row[16];
@@ -394,7 +348,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         // Two K blocks a turn: one wait and one address for both.
         const bool two = j + 1 < KB;
         const uint32_t s0 = it % kGrStages, s1 = (it + 1) % kGrStages, last = it + (two ? 1 : 0);
-        ok = mbar_wait_spin(&stage_free[last % kGrStages], ((last / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
+        ok = mbar_wait_spin(&S.done[last % kGrStages], ((last / kGrStages) & 1) ^ 1, a.timeout_ns, abort);
         if (!ok) break;
         uint8_t* st0 = ring + s0 * kGrStageBytes + dst0;
         uint8_t* st1 = ring + s1 * kGrStageBytes + dst0;
@@ -450,11 +404,11 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     int parity = 0, from = 0;
     bool ok = true;
     for (int t = first; t < total; t += step, parity ^= 1) {
-      const GrTile g = gr_tile<PAIR>(S, a.E, n_tiles, t, from, rank);
+      const GrTile g = gr_tile(S, a.E, t, from);
       from = g.e;
       const bool columns = SWIGLU || (128 * half < a.tile_n && a.tile_n * g.n + 128 * half < a.N);
       const bool live = 32 * quad < g.rows && columns;  // this warp has rows (and columns) to hold
-      const int p = g.p0 + max(0, min(row, g.rows - 1));
+      const int p = g.p0 + min(row, g.rows - 1);
       const int r = a.in_rows != nullptr ? __ldg(a.in_rows + p) : p;
       const bool bad = r < 0 || r >= a.a_rows;
       const int o = SWIGLU || a.out_rows == nullptr ? p : __ldg(a.out_rows + p);
@@ -567,7 +521,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // the other CTA may still write this one's stages and signal its mbarriers
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
@@ -648,21 +601,16 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   a.tile_n = !swiglu && tiles(128) <= sms ? 128 : 256;
   const long long most = tiles(a.tile_n);
   cudaLaunchConfig_t cfg = {};
-  const bool pair = g.R >= kGrPairRows * static_cast<long long>(g.E) && most >= static_cast<long long>(kGrPairWaves) * sms;
-  cfg.gridDim = dim3(static_cast<unsigned>(pair ? sms & ~1 : most < sms ? most : sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
   cfg.blockDim = dim3(kGrThreads);
   cfg.dynamicSmemBytes = kGrSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pair ? 2 : 1;
-  void (*kernel)(GrArgs) = swiglu ? (pair ? grouped_fp8_kernel<true, true> : grouped_fp8_kernel<true, false>)
-                                  : (pair ? grouped_fp8_kernel<false, true> : grouped_fp8_kernel<false, false>);
+  cfg.numAttrs = 1;
+  void (*kernel)(GrArgs) = swiglu ? grouped_fp8_kernel<true> : grouped_fp8_kernel<false>;
   if (!ensure_smem_attr(dev, reinterpret_cast<const void*>(kernel), kGrSmemBytes)) return FME_ECUDA;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "grouped fp8 launch: %s", cudaGetErrorString(err));

@@ -334,6 +334,45 @@ def test_grouped_long_launches(fme):
     assert np.array_equal(q, q[first[which]]) and np.array_equal(s, s[first[which]])
 
 
+@pytest.mark.parametrize("K", [640, 1024])
+def test_grouped_long_launches_of_many_k_blocks(fme, K):
+    """Hundreds of tiles a CTA, with and without four K blocks' scales in a 16-byte unit, rows by index and as whole
+    boxes. The rows are 50, so every expected row is one of 50 an expert; the two forms of the input agree bit for bit."""
+    counts = [7001, 0, 12999, 64]
+    E, N, I, rows = len(counts), 4224, 2048, 50
+    off = np.cumsum([0] + counts).astype(np.int32)
+    idx = np.random.default_rng(83).integers(0, rows, size=off[-1]).astype(np.int32)
+    which = np.repeat(np.arange(E), counts) * rows + idx
+    a, sa, w, sw, _, _ = _grouped_inputs([1] * E, K, N, rows, 84, False)
+    y, size = prompt.grouped_product(a, sa, w, sw, np.arange(E + 1, dtype=np.int32) * rows, np.tile(np.arange(rows), E))
+    da, dsa, dw, dsw, doff, didx = _dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off), _dev(idx)
+    got = fme.moe_grouped_gemm_fp8(da, dsa, dw, dsw, doff, in_rows=didx)
+    boxes = fme.moe_grouped_gemm_fp8(da[didx.long()], dsa[didx.long()], dw, dsw, doff)
+    assert torch.equal(got, boxes)
+    got = _np(got)
+    first = np.array([np.flatnonzero(which == k)[0] if (which == k).any() else -1 for k in range(E * rows)])
+    tol = (K // 128 + 8) * 2 * U * size + np.abs(y) * 2.0 ** -8 * 1.001
+    for k in np.flatnonzero(first >= 0):
+        assert np.all(np.abs(got[first[k]] - y[k]) <= tol[k])
+    assert np.array_equal(got, got[first[which]])
+
+    w13, s13 = dw[:, :2 * I].contiguous(), dsw[:, :2 * I // 128].contiguous()
+    q, s = fme.moe_grouped_swiglu_fp8(da, dsa, w13, s13, doff, in_rows=didx, limit=7.0)
+    qb, sb = fme.moe_grouped_swiglu_fp8(da[didx.long()], dsa[didx.long()], w13, s13, doff, limit=7.0)
+    assert torch.equal(q, qb) and torch.equal(s, sb)
+    q, s = _np(q), _np(s).astype(np.float64)
+    up, gate, su, sg = y[:, :I], y[:, I:2 * I], size[:, :I], size[:, I:2 * I]
+    h = clamped_swiglu(gate, up, 7.0)
+    du, dg = ((K // 128 + 8) * 2 * U * v for v in (su, sg))
+    g, u = np.minimum(gate, 7.0), np.clip(up, -7.0, 7.0)
+    dh = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + 16 * U * np.abs(h)
+    for k in np.flatnonzero(first >= 0):
+        base = np.maximum(np.abs(h[k]).reshape(-1, 128).max(-1), 1e-10) / 448
+        assert np.all(np.abs(s[first[k]] - base) <= dh[k].reshape(-1, 128).max(-1) / 448 + 4 * U * base)
+        _check_codes(q[first[k]], np.repeat(s[first[k]], 128), h[k], dh[k] + 4 * U * np.abs(h[k]))
+    assert np.array_equal(q, q[first[which]]) and np.array_equal(s, s[first[which]])
+
+
 def test_grouped_outputs_at_any_16_bytes(fme):
     a, sa, w, sw, off, _ = _grouped_inputs([70, 60], 256, 384, 130, 78, False)
     args = (_dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off))
