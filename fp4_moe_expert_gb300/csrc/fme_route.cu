@@ -17,6 +17,9 @@ namespace fme {
 
 constexpr int kRtMaxCtas = 152;
 constexpr int kRtTokens = 16;  // least tokens a CTA is given, where there are as many
+// Set in the arrival word by a CTA whose wait gave up or met a word that was not left clean: no later call of this
+// workspace takes stale counts for its own until the workspace is cleared.
+constexpr uint32_t kRtBroken = 1u << 30;
 constexpr int kRtIds = 64;     // picks of its run that a warp keeps in shared memory; the rest it reads back
 // Warps a CTA: 32 where a lane's experts (J) leave 64 registers enough, else 16.
 template <int J>
@@ -36,7 +39,7 @@ struct RtArgs {
   int32_t* tokens;
   uint16_t* counts;  // [CTAs][pitch]: a share holds fewer than 65,536 tokens, an expert at most one route of each
   uint32_t* err;
-  uint32_t* sync;  // CTAs arrived, CTAs past the wait; zero between calls
+  uint32_t* sync;  // CTAs arrived (and kRtBroken), CTAs past the wait; zero between calls
   unsigned long long timeout_ns;
 };
 
@@ -223,12 +226,15 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
       __threadfence();
       red_release_gpu_add(a.sync, 1u);
       const uint64_t begin = globaltimer_ns();
-      while (ld_acquire_gpu(a.sync) < static_cast<uint32_t>(G))
-        if (globaltimer_ns() - begin > a.timeout_ns) {
-          atomicOr(a.err, kErrCrossWait);
-          gave_up = 1;
-          break;
-        }
+      int arrived;
+      while ((arrived = static_cast<int>(ld_acquire_gpu(a.sync))) < G)
+        if (globaltimer_ns() - begin > a.timeout_ns) break;
+      // More than G: the word held something before this call's first arrival (the last CTA to arrive sees it at least).
+      if (arrived != G) {
+        atomicOr(a.err, kErrCrossWait);
+        atomicOr(a.sync, kRtBroken);
+        gave_up = 1;
+      }
       // The last CTA past the wait leaves both words zero for the next call.
       if (!gave_up && atomicAdd(a.sync + 1, 1u) == static_cast<uint32_t>(G) - 1u) {
         a.sync[0] = 0u;
@@ -236,7 +242,11 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
       }
     }
     __syncthreads();
-    if (gave_up) return;
+    if (gave_up) {
+      if (blockIdx.x == 0)  // groups without rows: the products that read them have nothing to do
+        for (int e = threadIdx.x; e <= a.E; e += kRtThreads) a.offsets[e] = 0;
+      return;
+    }
     // Eight experts a load; the CTAs' rows are dealt to as many threads as there are to a column.
     const int words = a.pitch / 8, lanes = kRtThreads / words, col = threadIdx.x % words, first = threadIdx.x / words;
     if (first < lanes) {
@@ -291,8 +301,12 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
       const int i = (t - t0) * a.top_k + lane;
       const int e = i < kRtIds ? picks[warp][i] : a.ids[r];  // this lane's own store
       const int place = u.start[e] + seen[warp][e]++;
-      a.rows[place] = r;
-      a.tokens[place] = t;
+      if (static_cast<uint32_t>(place) < static_cast<uint32_t>(a.T * a.top_k)) {
+        a.rows[place] = r;
+        a.tokens[place] = t;
+      } else {
+        atomicOr(a.err, kErrCrossWait);  // counts of another call: this one passed the wait before its own were there
+      }
     }
     __syncwarp();
   }

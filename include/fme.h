@@ -421,7 +421,12 @@ int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, lo
  *   [1, min(E, 32)]. NaN logits give picks that are distinct and in range.
  *   Every pointer 16-byte aligned. The workspace (see
  *   fme_moe_route_workspace) must be zeroed before its first use; a
- *   workspace sized for T serves every smaller T. Errors: FME_OK, FME_EINVAL,
+ *   workspace sized for T serves every smaller T. A call whose CTAs could not
+ *   meet within the wait limit sets error bit 2 of the workspace; its ids and
+ *   weights are valid, offsets, rows and tokens are not (nothing is written
+ *   outside them). Every later call whose CTAs meet (T above 16) does the same
+ *   until the workspace is cleared: reading the error word does not clear the
+ *   counters. Errors: FME_OK, FME_EINVAL,
  *   FME_EUNSUPPORTED, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA.
  */
 int fme_moe_route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale,
