@@ -67,6 +67,7 @@ struct GrArgs {
   int a_rows, R, out_n, K, N, E;
   int up0, gate0;  // first up / gate weight row (swiglu)
   int tile_n;      // weight rows a tile: 256, or 128 (gemm)
+  uint32_t most;   // tiles that ascending offsets make at most
   float limit;
   int ue8m0;
   int wide;  // out is 32-byte aligned: whole sectors a store
@@ -87,7 +88,7 @@ struct GrShared {
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  int warp_sum[kGrThreads / 32];
+  uint32_t warp_sum[kGrThreads / 32];
   int off[kMaxExperts + 1];     // group starts, clamped to [0, R] and ascending
   int tiles[kMaxExperts + 1];   // tiles before group e
   float amax[2][2][128];        // [tile parity][column half][row]
@@ -190,10 +191,11 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
   }
   griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
-  // Tiles before each group: every thread a few groups, then a block scan.
+  // Tiles before each group: every thread a few groups, then a block scan. A group has 2^25 tiles at most and a warp 96
+  // groups, so a warp's sum fits 32 bits; the warps' sums are cut at one more than ascending offsets can make.
   constexpr int kPer = (kMaxExperts + kGrThreads - 1) / kGrThreads;
   const int first = blockIdx.x, step = gridDim.x;
-  int own[kPer], sum = 0;
+  uint32_t own[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
@@ -207,26 +209,30 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
     }
     sum += own[i];
   }
-  int scan = sum;
+  uint32_t scan = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
     if (lane >= d) scan += v;
   }
-  if (lane == 31) S.warp_sum[warp] = scan;
+  if (lane == 31) S.warp_sum[warp] = min(scan, a.most + 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int before = scan - sum;
+  uint32_t before = scan - sum;
   for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
-    if (e <= a.E) S.tiles[e] = before;
+    if (e <= a.E) S.tiles[e] = static_cast<int>(before);
     before += own[i];
   }
   __syncthreads();
-  const int total = S.tiles[a.E];
+  int total = S.tiles[a.E];
+  if (static_cast<uint32_t>(total) > a.most) {  // the offsets overlap: nothing is computed
+    total = 0;
+    if (blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrRoute);
+  }
   const uint32_t tmem = S.tmem;
   const volatile int* abort = &S.abort;
   if (warp >= kGrAccWarps) reg_dec<kGrOtherRegs>();
@@ -600,6 +606,7 @@ int grouped_fp8(const GroupedFp8& g, void* workspace, size_t workspace_bytes, cu
   // activations once for twice the columns (256 of 7168 x 2048, 2 tokens 38.8 us instead of 44.6).
   a.tile_n = !swiglu && tiles(128) <= sms ? 128 : 256;
   const long long most = tiles(a.tile_n);
+  a.most = static_cast<uint32_t>(most);  // (2^18 + 2^10) row tiles of 128 weight tiles, or fewer
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
   cfg.blockDim = dim3(kGrThreads);

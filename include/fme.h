@@ -457,8 +457,10 @@ size_t fme_moe_route_workspace(int T, int E, int top_k);
  *   up to 16384, I a multiple of 128 up to 8192, E in [1, 1024], a_rows in
  *   [1, 2^25], limit > 0 (+inf allowed).
  * Places no group holds are left as they are. Offsets are clamped to [0, R]
- * on the device; an in_rows entry outside [0, a_rows) gives a row of zeros and
- * sets error bit 8 of the workspace. Pointers 16-byte aligned (offsets and
+ * on the device, a group that would end before it begins is empty, and
+ * offsets whose groups overlap so far that they hold more 128-row tiles than R
+ * rows make compute nothing and set error bit 8 of the workspace; an in_rows entry outside [0, a_rows) gives a row of zeros and
+ * sets bit 8, too. Pointers 16-byte aligned (offsets and
  * in_rows 4-byte). The workspace (fme_moe_grouped_fp8_workspace) must be
  * zeroed before its first use. Errors as fme_moe_route.
  */
@@ -498,8 +500,9 @@ int fme_workspace_clear(void* workspace, size_t workspace_bytes, void* stream);
 /*
  * Read and clear the device error word of a workspace (synchronises stream).
  * *code receives 0 or a bit set: 1 = a ring wait timed out, 2 = a cross-CTA
- * wait timed out, 4 = the producer could not drain its copies, 8 = an output
- * row index fell outside its tensor (the write was skipped). Returns
+ * wait timed out (fme_moe_route: or met counters that no call had left), 4 =
+ * the producer could not drain its copies, 8 = a row index fell outside its
+ * tensor or group offsets overlapped (the write was skipped). Returns
  * FME_ETIMEOUT when *code != 0, FME_OK otherwise.
  */
 int fme_workspace_error(void* workspace, int* code, void* stream);

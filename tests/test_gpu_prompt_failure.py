@@ -62,3 +62,25 @@ def test_route_stale_words_write_nothing_outside(fme, monkeypatch, preset):
         for b in bufs:
             assert (b[:guard] == -7).all() and (b[guard + n:] == -7).all()
             assert int(b.max()) < n
+
+
+@pytest.mark.parametrize("R,E,N", [(1000, 8, 256), (1 << 25, 1024, 16384)])
+def test_grouped_offsets_that_overlap(fme, R, E, N):
+    """Groups that hold every row again and again (at the larger size their tiles are more than 32 bits count): nothing
+    is computed, the error is reported, and ascending offsets run as before."""
+    K = 128
+    a = torch.full((1, K), 0x38, dtype=torch.uint8, device=DEV)  # ones
+    sa = torch.ones(1, 1, device=DEV)
+    w = torch.full((E, N, K), 0x38, dtype=torch.uint8, device=DEV)
+    sw = torch.ones(E, N // 128, 1, device=DEV)
+    rows = torch.zeros(R, dtype=torch.int32, device=DEV)
+    out = torch.full((1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = fme.Workspace(fme.moe_grouped_fp8_workspace(R, K, N, E), DEV)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[1::2] = R
+    fme.moe_grouped_gemm_fp8(a, sa, w, sw, off, in_rows=rows, out_rows=rows, out=out, workspace=ws)
+    assert ws.error() == 8 and (out == 7).all()
+    off[:] = 3
+    off[-1] = 4
+    fme.moe_grouped_gemm_fp8(a, sa, w, sw, off, in_rows=rows, out_rows=rows, out=out, workspace=ws)
+    assert ws.error() == 0 and (out == K).all()
