@@ -365,16 +365,16 @@ def ue8m0_unpack(packed, n, k, check=True):
 
 
 def _stream_workspace(nbytes, device, workspace):
-    """The caller's workspace, or one kept per device, current stream and size. During a graph capture a new one is the
-    graph's own: zeroed in every replay, and not kept for calls outside it."""
+    """The caller's workspace, or one kept per device, current stream and size. A graph capture gets a new one, the
+    graph's own: zeroed in every replay, and shared neither with calls outside the graph nor with another graph."""
     if workspace is not None:
         return _workspace(nbytes, device, workspace)
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(nbytes, device)
     key = (device.index, _stream(device), nbytes)
     ws = _ws_cache.get(key)
     if ws is None:
-        ws = Workspace(nbytes, device)
-        if not torch.cuda.is_current_stream_capturing():
-            _ws_cache[key] = ws
+        ws = _ws_cache[key] = Workspace(nbytes, device)
     return ws
 
 

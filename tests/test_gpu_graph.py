@@ -110,3 +110,40 @@ def test_nvfp4_layer_replay_matches_direct_calls(fme):
         _, gids, gw = box["r"]
         assert torch.equal(gids, rids) and torch.equal(gw, rw) and torch.equal(y, ry)
         assert ws.error() == 0
+
+
+def test_a_graph_captured_on_a_warmed_stream_has_its_own_workspace(fme, monkeypatch):
+    """Prompt calls without workspaces, run on a stream and then captured on it: the graph's launches get workspaces that
+    no call outside it uses, nor another graph, and replaying both beside calls on that stream gives what they give."""
+    T, E, k = 3000, 64, 4
+    logits, bias = torch.randn(T, E, device=DEV), torch.zeros(E, device=DEV)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    given = []
+    make = fme._stream_workspace
+    monkeypatch.setattr(fme, "_stream_workspace", lambda *a: given.append(make(*a)) or given[-1])
+    with torch.cuda.stream(s):
+        want = fme.moe_route(logits, bias, k)
+    s.synchronize()
+    graphs, results = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            results.append(fme.moe_route(logits, bias, k))
+        graphs.append(g)
+    eager, first, second = (w.buf.data_ptr() for w in given)
+    assert len({eager, first, second}) == 3
+    with torch.cuda.stream(s):  # the kept one still serves the stream
+        fme.moe_route(logits, bias, k)
+    assert given[-1].buf.data_ptr() == eager
+    torch.cuda.synchronize()
+    beside = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, b in zip(graphs, beside):
+            with torch.cuda.stream(b):
+                g.replay()
+        with torch.cuda.stream(s):
+            got = fme.moe_route(logits, bias, k)
+    torch.cuda.synchronize()
+    for r in (got, *results):
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
