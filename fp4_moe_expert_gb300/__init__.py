@@ -541,7 +541,14 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
     moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
 
     xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
-    weights these are. Returns (y [T, H] BF16, ids, weights); no tokens give empty ones."""
+    weights these are, and whose shapes are checked alike. Returns (y [T, H] BF16, ids, weights); no tokens give empty
+    ones."""
+    T, H = xq.shape
+    E, I = logits.shape[-1], w2.shape[-1]
+    for t, shape, name in ((sx, (T, H // 128), "sx"), (logits, (T, E), "logits"), (bias, (E,), "bias"),
+                           (w13, (E, 2 * I, H), "w13"), (w2, (E, H, I), "w2"), (shared_out, (T, H), "shared_out")):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
     ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale)
     hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0)
     out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows)

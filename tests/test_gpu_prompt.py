@@ -568,3 +568,24 @@ def test_prompt_layer_without_tokens_and_captured_without_workspaces(fme):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, fme.moe_prompt_fp8(q, s, logits, bias, *weights, *routed)[0])
+
+
+def test_prompt_layer_refuses_operands_that_disagree(fme):
+    """Tokens and logits of different counts, and weights of another shape, are refused before anything runs."""
+    cfg, T = W.RAGGED, 20
+    w13, s13, w2, s2 = _layer(cfg, 51)
+    q = torch.zeros(T, cfg.H, dtype=torch.uint8, device=DEV)
+    s = torch.ones(T, cfg.H // 128, device=DEV)
+    lg, bias = torch.randn(T, cfg.E, device=DEV), torch.zeros(cfg.E, device=DEV)
+    shared = torch.zeros(T, cfg.H, dtype=torch.bfloat16, device=DEV)
+    good = dict(xq=q, sx=s, logits=lg, bias=bias, w13=w13, s13=s13, w2=w2, s2=s2, top_k=cfg.top_k, limit=cfg.limit,
+                scale=cfg.scale, ue8m0=cfg.ue8m0, shared_out=shared)
+    fme.moe_prompt_fp8(**good)
+    for name, t in (("logits", lg[:-1]), ("logits", torch.cat([lg, lg[:1]])), ("logits", lg[0]), ("sx", s[1:]),
+                    ("bias", bias[1:]), ("w13", w13[1:]), ("w13", w13[:, :-256].contiguous()),
+                    ("w2", w2[:, :-128].contiguous()), ("w2", w2[1:]), ("shared_out", shared[1:])):
+        with pytest.raises(ValueError, match="expected"):
+            fme.moe_prompt_fp8(**{**good, name: t})
+    few = {**good, "xq": q[:-1], "sx": s[:-1]}
+    with pytest.raises(ValueError, match="logits"):
+        fme.moe_prompt_fp8(**few)
