@@ -107,7 +107,9 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _need(t, dtype, shape, name):
+def _need(t, dtype, shape, name, device=None):
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other operands on {device}")
     if t.dtype != dtype or t.shape != torch.Size(shape) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} contiguous={t.is_contiguous()} cuda={t.is_cuda}")
@@ -368,6 +370,8 @@ def _stream_workspace(nbytes, device, workspace):
     """The caller's workspace, or one kept per device, current stream and size. A graph capture gets a new one, the
     graph's own: zeroed in every replay, and shared neither with calls outside the graph nor with another graph."""
     if workspace is not None:
+        if workspace.buf.device != device:
+            raise ValueError(f"workspace: on {workspace.buf.device}, the operands on {device}")
         return _workspace(nbytes, device, workspace)
     if torch.cuda.is_current_stream_capturing():
         return Workspace(nbytes, device)
@@ -376,6 +380,13 @@ def _stream_workspace(nbytes, device, workspace):
     if ws is None:
         ws = _ws_cache[key] = Workspace(nbytes, device)
     return ws
+
+
+def _launch_stream(device):
+    """The current stream of the operands' device, which has to be the current device: kernels launch there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"operands on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(device)
 
 
 def _rows(t, name):
@@ -389,7 +400,7 @@ def _rows(t, name):
 def _out(t, shape, dtype, device, name):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, shape, name)
+    _need(t, dtype, shape, name, device)
     return t
 
 
@@ -400,12 +411,14 @@ def _addr(t):
 def _add_rmsnorm(x, gamma, residual, eps, mx, ue8m0, want_normed, q, scales, normed, residual_out):
     ldx, dev = _rows(x, "x"), x.device
     T, H = x.shape
-    _need(gamma, torch.bfloat16, (H,), "gamma")
+    _need(gamma, torch.bfloat16, (H,), "gamma", dev)
     ldr = H
     if residual is not None:
         ldr = _rows(residual, "residual")
         if residual.shape != x.shape:
             raise ValueError(f"residual: expected {tuple(x.shape)}, got {tuple(residual.shape)}")
+        if residual.device != dev:
+            raise ValueError(f"residual: on {residual.device}, the other operands on {dev}")
         residual_out = _out(residual_out, (T, H), torch.bfloat16, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
@@ -418,11 +431,11 @@ def _add_rmsnorm(x, gamma, residual, eps, mx, ue8m0, want_normed, q, scales, nor
     if mx:
         st = lib.fme_add_rmsnorm_mxfp8(x.data_ptr(), ldx, _addr(residual), ldr, gamma.data_ptr(), T, H, eps,
                                        q.data_ptr(), scales.data_ptr(), _addr(normed), _addr(residual_out),
-                                       _stream(dev))
+                                       _launch_stream(dev))
     else:
         st = lib.fme_add_rmsnorm_fp8(x.data_ptr(), ldx, _addr(residual), ldr, gamma.data_ptr(), T, H, eps,
                                      int(bool(ue8m0)), q.data_ptr(), scales.data_ptr(), _addr(normed),
-                                     _addr(residual_out), _stream(dev))
+                                     _addr(residual_out), _launch_stream(dev))
     _check(st)
     return q, scales, residual_out, normed
 
@@ -457,7 +470,7 @@ def moe_route(logits, bias, top_k, scale=1.0, ids=None, weights=None, offsets=No
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits must be float32 or bfloat16")
     _need(logits, logits.dtype, (T, E), "logits")
-    _need(bias, torch.float32, (E,), "bias")
+    _need(bias, torch.float32, (E,), "bias", dev)
     ids = _out(ids, (T, top_k), torch.int32, dev, "ids")
     weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
     offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets")
@@ -469,7 +482,7 @@ def moe_route(logits, bias, top_k, scale=1.0, ids=None, weights=None, offsets=No
     ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
     _check(lib.fme_moe_route(logits.data_ptr(), ldt, bias.data_ptr(), T, E, top_k, scale, ids.data_ptr(),
                              weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), tokens.data_ptr(),
-                             ws.buf.data_ptr(), ws.nbytes, _stream(dev)))
+                             ws.buf.data_ptr(), ws.nbytes, _launch_stream(dev)))
     return ids, weights, offsets, rows, tokens
 
 
@@ -482,14 +495,14 @@ def _need_grouped(a, sa, w, sw, offsets, in_rows):
     E, N, K = w.shape
     a_rows = a.shape[0]
     _need(a, torch.uint8, (a_rows, K), "a")
-    _need(sa, torch.float32, (a_rows, K // 128), "sa")
-    _need(w, torch.uint8, (E, N, K), "w")
-    _need(sw, torch.float32, (E, N // 128, K // 128), "sw")
-    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(sa, torch.float32, (a_rows, K // 128), "sa", a.device)
+    _need(w, torch.uint8, (E, N, K), "w", a.device)
+    _need(sw, torch.float32, (E, N // 128, K // 128), "sw", a.device)
+    _need(offsets, torch.int32, (E + 1,), "offsets", a.device)
     R = a_rows
     if in_rows is not None:
         R = in_rows.numel()
-        _need(in_rows, torch.int32, (R,), "in_rows")
+        _need(in_rows, torch.int32, (R,), "in_rows", a.device)
     return a_rows, K, E, N, R
 
 
@@ -512,7 +525,7 @@ def moe_grouped_swiglu_fp8(a, sa, w13, s13, offsets, in_rows=None, limit=float("
     _check(lib.fme_moe_grouped_swiglu_fp8(a.data_ptr(), sa.data_ptr(), a_rows, w13.data_ptr(), s13.data_ptr(),
                                           offsets.data_ptr(), _addr(in_rows), R, H, I, E, limit, int(bool(ue8m0)),
                                           int(bool(gate_first)), q.data_ptr(), scales.data_ptr(), ws.buf.data_ptr(),
-                                          ws.nbytes, _stream(dev)))
+                                          ws.nbytes, _launch_stream(dev)))
     return q, scales
 
 
@@ -523,16 +536,17 @@ def moe_grouped_gemm_fp8(a, sa, w, sw, offsets, in_rows=None, out_rows=None, out
     a_rows, K, E, N, R = _need_grouped(a, sa, w, sw, offsets, in_rows)
     dev = a.device
     if out_rows is not None:
-        _need(out_rows, torch.int32, (R,), "out_rows")
+        _need(out_rows, torch.int32, (R,), "out_rows", dev)
     if out is None:
         out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, (out.shape[0], N), "out")
+    _need(out, torch.bfloat16, (out.shape[0], N), "out", dev)
     if R == 0:
         return out
     ws = _stream_workspace(moe_grouped_fp8_workspace(R, K, N, E), dev, workspace)
     _check(lib.fme_moe_grouped_gemm_fp8(a.data_ptr(), sa.data_ptr(), a_rows, w.data_ptr(), sw.data_ptr(),
                                         offsets.data_ptr(), _addr(in_rows), _addr(out_rows), R, K, N, E,
-                                        out.data_ptr(), out.shape[0], ws.buf.data_ptr(), ws.nbytes, _stream(dev)))
+                                        out.data_ptr(), out.shape[0], ws.buf.data_ptr(), ws.nbytes,
+                                        _launch_stream(dev)))
     return out
 
 
@@ -549,6 +563,8 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
                            (w13, (E, 2 * I, H), "w13"), (w2, (E, H, I), "w2"), (shared_out, (T, H), "shared_out")):
         if t is not None and t.shape != shape:
             raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+        if t is not None and t.device != xq.device:
+            raise ValueError(f"{name}: on {t.device}, the other operands on {xq.device}")
     ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale)
     hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0)
     out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows)

@@ -7,7 +7,9 @@
  * - Pointers named x, logits, bias, w13, s13, w2, s2, topk_ids, topk_weights,
  *   packed (inputs) and out, ids, weights, y, gate_up, dst (outputs) are
  *   DEVICE pointers; the caller owns every buffer. The library never
- *   allocates, frees or caches device memory.
+ *   allocates, frees or caches device memory. Kernels launch on the current
+ *   device, whose own memory every pointer is (the prompt operators' binding
+ *   refuses tensors of another one).
  * - Matrices are dense row-major (last index fastest). Every device pointer
  *   must be 16-byte aligned.
  * - `stream` is a cudaStream_t passed as void* (NULL = legacy default

@@ -1,5 +1,6 @@
-"""Failure detection of the prompt operators, made on the host: a workspace whose words are preset so that a wait runs
-out or a meeting finds words that no call left. No kernel faults; each call returns, reports and stays in its buffers."""
+"""Failure detection of the prompt operators, made on the host: a workspace whose words are preset so that a wait
+runs out or a meeting finds words that no call left. No kernel faults; each call returns, reports and stays in its
+buffers."""
 
 import time
 

@@ -108,3 +108,71 @@ def test_binding_refuses_what_it_cannot_pass_on(fme):
     with pytest.raises(ValueError):
         fme.moe_grouped_gemm_fp8(a, s, torch.zeros(1, 128, 256, dtype=torch.uint8), torch.zeros(1, 1, 2),
                                  torch.zeros(2, dtype=torch.int32))
+
+
+class _Operand:
+    """What the binding asks of a tensor before it launches: enough to stand for one on a GPU that is not there."""
+
+    def __init__(self, dtype, *shape, gpu=0):
+        import torch
+        self.dtype, self.shape, self.device, self.is_cuda = dtype, torch.Size(shape), torch.device("cuda", gpu), True
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i=None):
+        s = [self.shape[j + 1:].numel() for j in range(len(self.shape))]
+        return tuple(s) if i is None else s[i]
+
+    def data_ptr(self):
+        return 16
+
+
+def test_binding_refuses_operands_of_two_devices(fme, monkeypatch):
+    import torch
+
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    T, H, E, I, k = 4, 256, 3, 128, 2
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ws, far = fme.Workspace.__new__(fme.Workspace), fme.Workspace.__new__(fme.Workspace)
+    ws.nbytes, ws.buf = 1 << 20, _Operand(u8, 1 << 20)
+    far.nbytes, far.buf = 1 << 20, _Operand(u8, 1 << 20, gpu=1)
+    calls = {
+        fme.add_rmsnorm_fp8: dict(x=(bf, T, H), gamma=(bf, H), residual=(bf, T, H), q=(u8, T, H), scales=(f32, T, 2),
+                                  normed=(bf, T, H), residual_out=(bf, T, H)),
+        fme.add_rmsnorm_mxfp8: dict(x=(bf, T, H), gamma=(bf, H), residual=(bf, T, H), q=(u8, T, H),
+                                    scales=(u8, T, 8), normed=(bf, T, H), residual_out=(bf, T, H)),
+        fme.moe_route: dict(logits=(f32, T, E), bias=(f32, E), ids=(i32, T, k), weights=(f32, T, k),
+                            offsets=(i32, E + 1), rows=(i32, T * k), tokens=(i32, T * k)),
+        fme.moe_grouped_swiglu_fp8: dict(a=(u8, T, H), sa=(f32, T, 2), w13=(u8, E, 2 * I, H), s13=(f32, E, 2, 2),
+                                         offsets=(i32, E + 1), in_rows=(i32, 8), q=(u8, 8, I), scales=(f32, 8, 1)),
+        fme.moe_grouped_gemm_fp8: dict(a=(u8, T, H), sa=(f32, T, 2), w=(u8, E, I, H), sw=(f32, E, 1, 2),
+                                       offsets=(i32, E + 1), in_rows=(i32, 8), out_rows=(i32, 8), out=(bf, 8, I)),
+        fme.moe_prompt_fp8: dict(xq=(u8, T, H), sx=(f32, T, 2), logits=(f32, T, E), bias=(f32, E),
+                                 w13=(u8, E, 2 * I, H), s13=(f32, E, 2, 2), w2=(u8, E, H, I), s2=(f32, E, 2, 1),
+                                 shared_out=(bf, T, H)),
+    }
+    more = {fme.moe_route: dict(top_k=k, workspace=ws), fme.moe_grouped_swiglu_fp8: dict(workspace=ws),
+            fme.moe_grouped_gemm_fp8: dict(workspace=ws),
+            fme.moe_prompt_fp8: dict(top_k=k, limit=7.0, scale=1.0, ue8m0=False)}
+    for fn, spec in calls.items():
+        rest = more.get(fn, {})
+        if fn is not fme.moe_prompt_fp8:  # everything on one device, but not the current one
+            elsewhere = {**rest, "workspace": far} if "workspace" in rest else rest
+            with pytest.raises(ValueError, match="current device"):
+                fn(**{n: _Operand(*v, gpu=1) for n, v in spec.items()}, **elsewhere)
+            if "workspace" in rest:
+                with pytest.raises(ValueError, match="workspace"):
+                    fn(**{n: _Operand(*v) for n, v in spec.items()}, **elsewhere)
+        for name in spec:
+            if fn is fme.moe_prompt_fp8 and name in ("s13", "s2"):
+                continue  # the products refuse those
+            with pytest.raises(ValueError, match="cuda:1"):
+                fn(**{n: _Operand(*v, gpu=int(n == name)) for n, v in spec.items()}, **rest)
