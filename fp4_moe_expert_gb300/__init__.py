@@ -152,6 +152,23 @@ def _workspace(nbytes, device, workspace):
     return ws
 
 
+def kept_workspace_error(device=None):
+    """Device error bits (Workspace.error, or-ed; 0 = none) of the workspaces kept for calls that were given none, on
+    `device` (default: the current one). Synchronises the device. A workspace with an error is cleared, so that later
+    calls are right again; what the calls since the error returned is not."""
+    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    torch.cuda.synchronize(index)
+    bits = 0
+    for key, ws in _ws_cache.items():
+        if key[0] == index:
+            code = ws.error()
+            if code != 0:
+                ws.clear()
+            bits |= code
+    torch.cuda.synchronize(index)
+    return bits
+
+
 def moe_routed_fp8_workspace(M, H, I, E, top_k):
     return lib.fme_moe_routed_fp8_workspace(M, H, I, E, top_k)
 
@@ -550,13 +567,23 @@ def moe_grouped_gemm_fp8(a, sa, w, sw, offsets, in_rows=None, out_rows=None, out
     return out
 
 
-def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, shared_out=None):
+def moe_prompt_workspaces(T, H, I, E, top_k, device):
+    """The workspaces of moe_prompt_fp8 (routing, gate/up and down product) for up to T tokens."""
+    R = T * top_k
+    return (Workspace(moe_route_workspace(T, E, top_k), device),
+            Workspace(moe_grouped_fp8_workspace(R, H, 2 * I, E), device),
+            Workspace(moe_grouped_fp8_workspace(R, I, H, E), device))
+
+
+def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, shared_out=None,
+                   workspaces=None):
     """The routed FP8 experts of a prompt of T tokens, combined: moe_route, moe_grouped_swiglu_fp8 on the tokens' rows,
     moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
 
     xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
     weights these are, and whose shapes are checked alike. Returns (y [T, H] BF16, ids, weights); no tokens give empty
-    ones."""
+    ones. Without workspaces (moe_prompt_workspaces) the binding's kept ones serve, whose device errors
+    kept_workspace_error reads; a graph that is to report its errors needs workspaces of the caller's."""
     T, H = xq.shape
     E, I = logits.shape[-1], w2.shape[-1]
     for t, shape, name in ((sx, (T, H // 128), "sx"), (logits, (T, E), "logits"), (bias, (E,), "bias"),
@@ -565,9 +592,11 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
             raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
         if t is not None and t.device != xq.device:
             raise ValueError(f"{name}: on {t.device}, the other operands on {xq.device}")
-    ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale)
-    hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0)
-    out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows)
+    ws = workspaces or (None, None, None)
+    ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale, workspace=ws[0])
+    hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0,
+                                    workspace=ws[1])
+    out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows, workspace=ws[2])
     if xq.shape[0] == 0:
         return out, ids, weights
     return moe_finalize(out, weights, shared_out), ids, weights

@@ -7,6 +7,8 @@ import time
 import pytest
 import torch
 
+from synth import workloads as W
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 SYNC = 64  # byte of the arrival word in moe_route's workspace, the count of CTAs past the wait behind it
@@ -85,3 +87,50 @@ def test_grouped_offsets_that_overlap(fme, R, E, N):
     off[-1] = 4
     fme.moe_grouped_gemm_fp8(a, sa, w, sw, off, in_rows=rows, out_rows=rows, out=out, workspace=ws)
     assert ws.error() == 0 and (out == K).all()
+
+
+def _prompt(T):
+    cfg = W.RAGGED
+    w13h, w2h = W.fp8_weights_host(cfg, 61)
+    s13, s2 = W.fp8_weight_scales(cfg, 61)
+    weights = [torch.from_numpy(v).to(DEV) for v in (w13h.full(), s13, w2h.full(), s2)]
+    q = torch.randint(0, 0x7F, (T, cfg.H), dtype=torch.uint8, device=DEV)
+    s = torch.rand(T, cfg.H // 128, device=DEV) * 2.0 ** -8
+    logits, bias = torch.randn(T, cfg.E, device=DEV), torch.zeros(cfg.E, device=DEV)
+    return cfg, (q, s, logits, bias, *weights, cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0)
+
+
+def test_prompt_errors_are_read_and_cleared_on_the_default_path(fme, monkeypatch):
+    cfg, args = _prompt(200)
+    want = fme.moe_prompt_fp8(*args)
+    assert fme.kept_workspace_error() == 0 and fme.kept_workspace_error(DEV) == 0
+    kept = fme._stream_workspace(fme.moe_route_workspace(200, cfg.E, cfg.top_k), torch.device(DEV), None)
+    monkeypatch.setenv("FME_WAIT_TIMEOUT_MS", "20")
+    _preset(kept, -1)
+    fme.moe_prompt_fp8(*args)
+    fme.moe_prompt_fp8(*args)
+    assert fme.kept_workspace_error() == 2
+    assert not kept.buf[:256].any() and fme.kept_workspace_error() == 0
+    got = fme.moe_prompt_fp8(*args)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and fme.kept_workspace_error() == 0
+
+
+def test_prompt_with_the_callers_workspaces(fme, monkeypatch):
+    cfg, args = _prompt(200)
+    want = fme.moe_prompt_fp8(*args)
+    ws = fme.moe_prompt_workspaces(300, cfg.H, cfg.I, cfg.E, cfg.top_k, DEV)  # they serve fewer tokens, too
+    kept = dict(fme._ws_cache)
+    got = fme.moe_prompt_fp8(*args, workspaces=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and [w.error() for w in ws] == [0, 0, 0]
+    monkeypatch.setenv("FME_WAIT_TIMEOUT_MS", "20")
+    _preset(ws[0], -1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, _, _ = fme.moe_prompt_fp8(*args, workspaces=ws)
+    assert set(fme._ws_cache) == set(kept)
+    g.replay()
+    assert [w.error() for w in ws] == [2, 0, 0]
+    ws[0].clear()
+    g.replay()
+    assert [w.error() for w in ws] == [0, 0, 0] and torch.equal(y, want[0])
+    assert fme.kept_workspace_error() == 0
