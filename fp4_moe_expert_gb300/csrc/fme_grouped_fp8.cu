@@ -465,8 +465,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
         if (live) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) {
-            const float up = fminf(fmaxf(acc[c], -a.limit), a.limit);
-            const float gate = fminf(acc[64 + c], a.limit);
+            const float up = min_nan(max_nan(acc[c], -a.limit), a.limit);
+            const float gate = min_nan(acc[64 + c], a.limit);
             acc[c] = __fmul_rn(silu(gate), up);
             amax = fmaxf(amax, fabsf(acc[c]));
           }

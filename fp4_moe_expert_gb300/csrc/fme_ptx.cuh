@@ -216,6 +216,18 @@ __device__ __forceinline__ float recip_rn(float d) {
   return __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
 }
 
+// The smaller / larger of two, NaN when either is (fminf and fmaxf leave NaN out).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Monotone uint32 key of a float (negative: all bits flipped; else the sign
 // bit set), so unsigned order equals float order for non-NaN values.
 __device__ __forceinline__ uint32_t ordered_key(float v) {

@@ -458,6 +458,9 @@ size_t fme_moe_route_workspace(int T, int E, int top_k);
  *   [R, I/128] FP32. R in [0, 2^25] (0: nothing is done), H a multiple of 128
  *   up to 16384, I a multiple of 128 up to 8192, E in [1, 1024], a_rows in
  *   [1, 2^25], limit > 0 (+inf allowed).
+ * A product that is NaN (a NaN code or scale) gives a NaN code, also through
+ * the clamps; the block's scale is that of its other values. (The decode
+ * entry points' clamps turn a NaN gate or up value into the limit.)
  * Places no group holds are left as they are. Offsets are clamped to [0, R]
  * on the device, a group that would end before it begins is empty, and
  * offsets whose groups overlap so far that they hold more 128-row tiles than R

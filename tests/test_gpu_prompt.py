@@ -589,3 +589,27 @@ def test_prompt_layer_refuses_operands_that_disagree(fme):
     few = {**good, "xq": q[:-1], "sx": s[:-1]}
     with pytest.raises(ValueError, match="logits"):
         fme.moe_prompt_fp8(**few)
+
+
+@pytest.mark.parametrize("limit", [7.0, float("inf")])
+def test_grouped_swiglu_keeps_nan(fme, limit):
+    """A NaN token, token scale, gate weight or up weight makes NaN codes where it enters, and nothing else changes."""
+    H, I, R = 256, 256, 40
+    a, sa, w, sw, off, _ = _grouped_inputs([25, 15], H, 2 * I, R, 91, False)
+    da, dsa, dw, dsw, doff = _dev(a), _dev(sa), _dev(w), _dev(sw), _dev(off)
+    q, s = fme.moe_grouped_swiglu_fp8(da, dsa, dw, dsw, doff, limit=limit)
+    assert not ((q & 0x7F) == 0x7F).any()
+    bad, bad_s = da.clone(), dsa.clone()
+    bad[3, 17] = 0x7F
+    bad_s[30, 1] = float("nan")
+    qt, st = fme.moe_grouped_swiglu_fp8(bad, bad_s, dw, dsw, doff, limit=limit)
+    keep = [i for i in range(R) if i not in (3, 30)]
+    assert torch.equal(qt[keep], q[keep]) and torch.equal(st[keep], s[keep])
+    assert ((qt[[3, 30]] & 0x7F) == 0x7F).all()
+    wb = dw.clone()
+    wb[0, 5, 100] = 0xFF       # up row 5 of the first expert
+    wb[1, I + 140, 9] = 0x7F   # gate row 140 of the second
+    qw, _ = fme.moe_grouped_swiglu_fp8(da, dsa, wb, dsw, doff, limit=limit)
+    nan = (qw & 0x7F) == 0x7F
+    assert nan[:25, 5].all() and nan[25:, 140].all() and int(nan.sum()) == R
+    assert torch.equal(qw[:25, 128:], q[:25, 128:]) and torch.equal(qw[25:, :128], q[25:, :128])
