@@ -63,6 +63,7 @@ SIGNATURES = {
     "fme_moe_grouped_fp8_workspace": (_c_size, [_c_int] * 4),
     "fme_workspace_clear": (_c_int, [_vp, _c_size, _vp]),
     "fme_selftest_wait_timeout": (_c_int, [_vp, _c_size, _c_int, _vp]),
+    "fme_selftest_rounding": (_c_int, [_c_int, ctypes.c_uint32, ctypes.c_ulonglong, _vp, _vp]),
     "fme_workspace_error": (_c_int, [_vp, ctypes.POINTER(_c_int), _vp]),
     "fme_sm_count": (_c_int, []),
 }

@@ -111,6 +111,40 @@ __global__ void selftest_wait_kernel(uint32_t* word, const uint32_t* flag, unsig
   }
 }
 
+// Counts where the short forms of fme_ptx.cuh differ from the general operations (NaN equal to NaN): item i is the float
+// of bits first + i, or (quotients) a pair of a divisor and a dividend drawn from a hash of first + i.
+__global__ void selftest_rounding_kernel(int what, uint32_t first, unsigned long long count,
+                                         unsigned long long* mismatches) {
+  unsigned long long bad = 0;
+  for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(blockDim.x) + threadIdx.x; i < count;
+       i += static_cast<unsigned long long>(gridDim.x) * blockDim.x) {
+    const uint32_t bits = first + static_cast<uint32_t>(i);
+    const float x = __uint_as_float(bits);
+    float got, want;
+    if (what == 0) {
+      got = recip_rn(x);
+      want = __fdiv_rn(1.0f, x);
+    } else if (what == 1) {
+      got = silu_rn(x);
+      want = __fdiv_rn(x, __fadd_rn(1.0f, expf(-x)));
+    } else {
+      // SplitMix64's output function (Steele, Lea and Flood 2014). Divisors in [2^-41, 2^23), dividends 2^-48 to 2^8 of them.
+      unsigned long long z = (static_cast<unsigned long long>(bits) + 1ull) * 0x9E3779B97F4A7C15ull;
+      z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+      z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+      z ^= z >> 31;
+      const uint32_t es = 127 - 41 + static_cast<uint32_t>(z >> 58);
+      const uint32_t eh = es - 48 + static_cast<uint32_t>((z >> 46) & 0xFFFu) % 57u;
+      const float s = __uint_as_float((es << 23) | (static_cast<uint32_t>(z) & 0x7FFFFFu));
+      const float h = __uint_as_float((eh << 23) | (static_cast<uint32_t>(z >> 23) & 0x7FFFFFu));
+      got = quotient_rn(h, s, __fdiv_rn(1.0f, s));
+      want = __fdiv_rn(h, s);
+    }
+    if (__float_as_uint(got) != __float_as_uint(want) && !(got != got && want != want)) ++bad;
+  }
+  if (bad != 0) atomicAdd(mismatches, bad);
+}
+
 }  // namespace fme
 
 using namespace fme;
@@ -574,6 +608,18 @@ int fme_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int timeo
   const uint32_t* flag = reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(workspace) + 256);
   selftest_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
       word, flag, static_cast<unsigned long long>(timeout_ms) * 1000000ull);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return set_last_error(FME_ECUDA, "selftest launch: %s", cudaGetErrorString(err));
+  return FME_OK;
+}
+
+int fme_selftest_rounding(int what, uint32_t first, unsigned long long count, unsigned long long* mismatches,
+                          void* stream) {
+  FME_REQUIRE(what >= 0 && what <= 2 && mismatches != nullptr, FME_EINVAL, "what=%d outside [0, 2], or a null pointer",
+              what);
+  FME_REQUIRE(count >= 1 && count <= (1ull << 32), FME_EINVAL, "count=%llu outside [1, 2^32]", count);
+  FME_REQUIRE((reinterpret_cast<uintptr_t>(mismatches) & 7u) == 0, FME_EALIGN, "mismatches must be 8-byte aligned");
+  selftest_rounding_kernel<<<1024, 256, 0, static_cast<cudaStream_t>(stream)>>>(what, first, count, mismatches);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "selftest launch: %s", cudaGetErrorString(err));
   return FME_OK;

@@ -137,18 +137,6 @@ __device__ __forceinline__ int gr_row(const GrArgs& a, const GrTile& g, int i) {
   return r >= 0 && r < a.a_rows ? r : 0;
 }
 
-// h / s correctly rounded, from inv = 1 / s correctly rounded: one residual step on the product (Markstein 1990).
-// Exact for the quotients of a block, |h / s| <= 448; where a tiny h makes the residual underflow, the code is zero.
-__device__ __forceinline__ float quotient(float h, float s, float inv) {
-  const float q = __fmul_rn(h, inv);
-  return __fmaf_rn(__fmaf_rn(-q, s, h), inv, q);
-}
-// g / (1 + exp(-g)) with the decode kernel's roundings (expf, a rounded quotient): equal for every float above -80.
-// Below, where the exact value is under 1e-33 and its E4M3 code zero, exp stays at exp(80), in recip_rn's range.
-__device__ __forceinline__ float silu(float g) {
-  const float d = __fadd_rn(1.0f, expf(fminf(-g, 80.0f)));
-  return quotient(g, d, recip_rn(d));
-}
 // (lo, hi) rounded to BF16, lo in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
@@ -467,7 +455,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           for (int c = 0; c < 64; ++c) {
             const float up = min_nan(max_nan(acc[c], -a.limit), a.limit);
             const float gate = min_nan(acc[64 + c], a.limit);
-            acc[c] = __fmul_rn(silu(gate), up);
+            acc[c] = __fmul_rn(silu_rn(gate), up);
             amax = fmaxf(amax, fabsf(acc[c]));
           }
         }
@@ -487,7 +475,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_fp8_kernel(const __grid
           for (int i = 0; i < 16; ++i) {
             float v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = quotient(acc[4 * i + k], s, inv);
+            for (int k = 0; k < 4; ++k) v[k] = quotient_rn(acc[4 * i + k], s, inv);
             w[i] = f32x2_to_e4m3x2(v[0], v[1]) | (f32x2_to_e4m3x2(v[2], v[3]) << 16);
           }
           const int I = a.N / 2;

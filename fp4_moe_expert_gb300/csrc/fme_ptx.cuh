@@ -208,12 +208,27 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(lo & 0xFFFF)));
 }
 
-// 1 / d for 1 <= d <= 2^125, correctly rounded (equal to __fdiv_rn(1, d) for every float of the range): one Newton
-// step on the hardware's approximation, a third of the instructions of the general division.
+// 1 / d for 2^-4 <= d <= 2^125, correctly rounded (equal to __fdiv_rn(1, d) for every float of the range, which the
+// rounding self-test sweeps): one Newton step on the hardware's approximation, whose residual 1 - d r the fused
+// multiply-add gives exactly (Markstein 1990); a third of the instructions of the general division.
 __device__ __forceinline__ float recip_rn(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
+}
+// h / s correctly rounded, from inv = 1 / s correctly rounded: one residual step on the product (Markstein 1990; run once
+// over all 2^46 pairs of mantissas). For finite quotients whose residual, 2^-24 of h, does not underflow.
+__device__ __forceinline__ float quotient_rn(float h, float s, float inv) {
+  const float q = __fmul_rn(h, inv);
+  return __fmaf_rn(-__fmaf_rn(q, s, -h), inv, q);  // (a residual of +0, taken off: -0 stays -0)
+}
+// g / (1 + exp(-g)) with the decode kernels' roundings (expf, a rounded quotient): equal for every float. The quotient
+// is taken by a sixteenth of the divisor, so that its reciprocal is normal up to where expf overflows; above 2^100 the
+// divisor is one, below -88.72 infinite.
+__device__ __forceinline__ float silu_rn(float g) {
+  const float d16 = __fmul_rn(__fadd_rn(1.0f, expf(-g)), 0.0625f);
+  const float v = __fmul_rn(quotient_rn(g, d16, recip_rn(d16)), 0.0625f);
+  return g >= -88.72283f && g <= 0x1p100f ? v : __fmul_rn(g, g > 0.0f ? 1.0f : 0.0f);
 }
 
 // The smaller / larger of two, NaN when either is (fminf and fmaxf leave NaN out).

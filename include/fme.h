@@ -459,7 +459,8 @@ size_t fme_moe_route_workspace(int T, int E, int top_k);
  *   up to 16384, I a multiple of 128 up to 8192, E in [1, 1024], a_rows in
  *   [1, 2^25], limit > 0 (+inf allowed).
  * A product that is NaN (a NaN code or scale) gives a NaN code, also through
- * the clamps; the block's scale is that of its other values. (The decode
+ * the clamps; the block's scale is that of its other values. A hidden value
+ * that overflows FP32 makes its block's scale infinite and its codes NaN. (The decode
  * entry points' clamps turn a NaN gate or up value into the limit.)
  * Places no group holds are left as they are. Offsets are clamped to [0, R]
  * on the device, a group that would end before it begins is empty, and
@@ -522,6 +523,18 @@ int fme_workspace_error(void* workspace, int* code, void* stream);
  * with fme_workspace_error. workspace_bytes >= 512, timeout_ms in [1, 10000].
  */
 int fme_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int timeout_ms, void* stream);
+
+/*
+ * Self-test of the kernels' short arithmetic forms (no counterpart in the
+ * pages): adds to *mismatches (device, 8-byte aligned) how many of `count`
+ * items differ from the general operations. what = 0: reciprocals of the floats
+ * whose bits are first, first + 1, ... (right for [2^-4, 2^125]); 1: SiLU of
+ * those floats against g / (1 + expf(-g)) with a rounded quotient (every
+ * float); 2: quotients of pairs hashed from first, first + 1, ... count in
+ * [1, 2^32]. Asynchronous on `stream`.
+ */
+int fme_selftest_rounding(int what, uint32_t first, unsigned long long count, unsigned long long* mismatches,
+                          void* stream);
 
 /* Number of streaming multiprocessors the kernels size their grids to. */
 int fme_sm_count(void);
