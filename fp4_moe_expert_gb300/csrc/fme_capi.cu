@@ -92,10 +92,13 @@ int ue8m0_unpack(const int32_t* packed, int n, int k, float* dst, int check, int
 }
 
 // Bounded-wait self-test: waits, each with the kernels' own primitives and a
-// time limit, on a global flag nothing sets and on an mbarrier nothing
-// arrives at; both must give up, set their error bits and return.
+// time limit, on a global flag nothing sets and on mbarriers nothing arrives
+// at (the decode kernels' wait, the grouped products' sleeping one, alone and
+// for two barriers of which one is complete); all must give up, the mbarrier
+// waits' bit is set only when each did, and a raised abort flag ends a wait.
 __global__ void selftest_wait_kernel(uint32_t* word, const uint32_t* flag, unsigned long long timeout_ns) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, complete;
+  __shared__ int abort;
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer_ns();
     while (ld_acquire_gpu(flag) == 0u) {
@@ -107,7 +110,16 @@ __global__ void selftest_wait_kernel(uint32_t* word, const uint32_t* flag, unsig
     }
     mbar_init(&bar, 1);
     fence_mbar_init();
-    if (!mbar_wait(&bar, 0, timeout_ns, nullptr)) atomicOr(word, kErrRingWait);
+    mbar_init(&complete, 1);
+    fence_mbar_init();
+    mbar_arrive(&complete);
+    abort = 1;
+    const volatile int* raised = &abort;
+    const bool waited = mbar_wait(&bar, 0, timeout_ns, nullptr) || mbar_wait_spin(&bar, 0, timeout_ns, nullptr) ||
+                        mbar_wait_spin2(&complete, 0, &bar, 0, timeout_ns, nullptr) ||
+                        mbar_wait_spin2(&bar, 0, &complete, 0, 20000000000ull, raised) ||
+                        !mbar_wait_spin2(&complete, 0, &complete, 0, timeout_ns, nullptr);
+    if (!waited) atomicOr(word, kErrRingWait);
   }
 }
 

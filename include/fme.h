@@ -460,8 +460,8 @@ size_t fme_moe_route_workspace(int T, int E, int top_k);
  *   [1, 2^25], limit > 0 (+inf allowed).
  * A product that is NaN (a NaN code or scale) gives a NaN code, also through
  * the clamps; the block's scale is that of its other values. A hidden value
- * that overflows FP32 makes its block's scale infinite and its codes NaN. (The decode
- * entry points' clamps turn a NaN gate or up value into the limit.)
+ * that overflows FP32 makes its block's scale infinite and its codes NaN. (The
+ * decode entry points' clamps turn a NaN gate or up value into the limit.)
  * Places no group holds are left as they are. Offsets are clamped to [0, R]
  * on the device, a group that would end before it begins is empty, and
  * offsets whose groups overlap so far that they hold more 128-row tiles than R
@@ -517,9 +517,10 @@ int fme_workspace_error(void* workspace, int* code, void* stream);
  * Self-test of the device-side bounded waits (no counterpart in the pages,
  * whose flag waits poll without a limit). Launches one small kernel that
  * waits, with the same primitives and a timeout_ms limit as the layer kernels,
- * on a flag nobody sets (workspace byte 256, which must be zero) and on an
- * mbarrier nobody arrives at. Both waits give up and set error bits 2 and 1
- * of the workspace error word; the GPU context stays usable. Read the result
+ * on a flag nobody sets (workspace byte 256, which must be zero) and, in three
+ * forms, on an mbarrier nobody arrives at. The waits give up one after another
+ * (4 timeout_ms in all) and set error bits 2 and 1 of the workspace error word,
+ * 1 only when every mbarrier wait did; the GPU context stays usable. Read the result
  * with fme_workspace_error. workspace_bytes >= 512, timeout_ms in [1, 10000].
  */
 int fme_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int timeout_ms, void* stream);

@@ -134,3 +134,15 @@ def test_prompt_with_the_callers_workspaces(fme, monkeypatch):
     g.replay()
     assert [w.error() for w in ws] == [0, 0, 0] and torch.equal(y, want[0])
     assert fme.kept_workspace_error() == 0
+
+
+def test_every_form_of_the_bounded_wait_runs_out(fme):
+    """The flag's wait and the mbarrier waits of the decode and the grouped kernels (one barrier, two), one after another."""
+    ws = fme.Workspace(512, DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert fme.lib.fme_selftest_wait_timeout(ws.ptr(), 512, 50, stream) == 0
+    ws.error(), ws.clear()  # loaded
+    t0 = time.perf_counter()
+    assert fme.lib.fme_selftest_wait_timeout(ws.ptr(), 512, 50, stream) == 0
+    assert ws.error() == 3
+    assert 0.2 <= time.perf_counter() - t0 < 5.0
