@@ -64,20 +64,28 @@ __global__ void __launch_bounds__(kFinThreads) finalize_kernel(const __nv_bfloat
 
 int finalize(const void* out, const float* weights, const void* shared_out, int M, int H, int top_k, void* y,
              cudaStream_t st) {
-  const long long items = static_cast<long long>(M) * (H / 8);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kFinThreads - 1) / kFinThreads));
-  cfg.blockDim = dim3(kFinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t err =
-      cudaLaunchKernelEx(&cfg, finalize_kernel, static_cast<const __nv_bfloat16*>(out), weights,
-                         static_cast<const __nv_bfloat16*>(shared_out), M, H, top_k, static_cast<__nv_bfloat16*>(y));
-  if (err != cudaSuccess) return set_last_error(FME_ECUDA, "finalize kernel launch: %s", cudaGetErrorString(err));
+  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(out);
+  const __nv_bfloat16* shared = static_cast<const __nv_bfloat16*>(shared_out);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(y);
+  // The kernel counts its items in 32 bits: one launch holds 2^30 of them (a prompt of 2^20 tokens, H = 16384: two).
+  const int step = (1 << 30) / (H / 8);
+  for (int t = 0; t < M; t += step) {
+    const int n = M - t < step ? M - t : step;
+    const long long items = static_cast<long long>(n) * (H / 8);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((items + kFinThreads - 1) / kFinThreads));
+    cfg.blockDim = dim3(kFinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(
+        &cfg, finalize_kernel, o + static_cast<size_t>(t) * top_k * H, weights + static_cast<size_t>(t) * top_k,
+        shared != nullptr ? shared + static_cast<size_t>(t) * H : nullptr, n, H, top_k, dst + static_cast<size_t>(t) * H);
+    if (err != cudaSuccess) return set_last_error(FME_ECUDA, "finalize kernel launch: %s", cudaGetErrorString(err));
+  }
   return FME_OK;
 }
 

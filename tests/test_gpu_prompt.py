@@ -613,3 +613,18 @@ def test_grouped_swiglu_keeps_nan(fme, limit):
     nan = (qw & 0x7F) == 0x7F
     assert nan[:25, 5].all() and nan[25:, 140].all() and int(nan.sum()) == R
     assert torch.equal(qw[:25, 128:], q[:25, 128:]) and torch.equal(qw[25:, :128], q[25:, :128])
+
+
+def test_finalize_of_the_longest_prompt(fme):
+    """2^20 tokens of 16384 values, more 16-byte items than 31 bits count: every row is combined."""
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("needs 70 GB")
+    T, H = 1 << 20, 16384
+    out = torch.ones(T, H, dtype=torch.bfloat16, device=DEV)
+    w = (torch.arange(T, device=DEV) % 251 + 1).float()[:, None]
+    y = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    fme.moe_finalize(out, w, y=y)
+    for part in range(0, T, 1 << 16):
+        assert (y[part:part + (1 << 16)] == w[part:part + (1 << 16)].bfloat16()).all()
+    del out, y
+    torch.cuda.empty_cache()
