@@ -628,3 +628,32 @@ def test_finalize_of_the_longest_prompt(fme):
         assert (y[part:part + (1 << 16)] == w[part:part + (1 << 16)].bfloat16()).all()
     del out, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 3), (64, 8), (65, 8), (200, 32), (256, 8), (257, 5), (512, 8), (513, 16),
+                                 (896, 16), (1024, 32)])
+def test_route_equals_the_decode_kernel_bit_for_bit(fme, E, k, bf16):
+    """Picks and weights of one long call against the decode kernel's of 64 tokens each: ordinary logits, logits whose
+    scores saturate or underflow, equal logits, and infinities."""
+    H, I, T = 128, 128, 320
+    g = torch.Generator(device=DEV).manual_seed(E + k)
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    logits[64:128] *= 40.0
+    logits[128:192] = logits[128:192].round()
+    logits[192:200] = 0.25
+    logits[200:208] -= 87.0
+    logits[208:212, ::3] = float("inf")
+    logits[212:216, ::2] = -float("inf")
+    logits[216:220] = -200.0
+    bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+    if bf16:
+        logits = logits.bfloat16()
+    zeros = [torch.zeros(s, dtype=d, device=DEV) for s, d in (((E, 2 * I, H), torch.uint8), ((E, 2, 1), torch.float32),
+                                                               ((E, H, I), torch.uint8), ((E, 1, 1), torch.float32))]
+    x = torch.zeros(64, H, dtype=torch.bfloat16, device=DEV)
+    ids, w = fme.moe_route(logits, bias, k, 2.5)[:2]
+    for t in range(0, T, 64):
+        _, di, dw = fme.moe_routed_fp8(x, logits[t:t + 64], bias, *zeros, k, 7.0, 2.5, False)
+        assert torch.equal(ids[t:t + 64], di)
+        assert torch.equal(w[t:t + 64].nan_to_num(-1.0).view(torch.int32), dw.nan_to_num(-1.0).view(torch.int32))
