@@ -16,8 +16,8 @@
 // the MMA, 10-11 copy activation rows by index.
 // * Loads: per 128-value K block two 128-row boxes of weights by TMA, and the tile's
 //   rows: a full tile of consecutive rows as one box, others row by row with cp.async
-//   (only the rows the group has; two warps, whose pace tells: predicates on a full tile cost 3 %). TMA's own row gather (tile::gather4) measured
-//   90 clocks for four rows, 2900 a tile and K block against 512 of MMA work.
+//   (only the rows the group has; two warps, whose pace tells: predicates on a full tile cost 3 %). TMA's own row gather
+//   (tile::gather4) measured 90 clocks for four rows, 2900 a tile and K block against 512 of MMA work.
 // * The scales are FP32 and not powers of two, so the MMA cannot apply them: each
 //   K block is one 128 x 256 accumulation in tensor memory (two buffers), and the
 //   accumulate warps add D * (sw * sa) into 128 registers a thread. A row is a
@@ -25,10 +25,12 @@
 // * Why 128 x 256: the largest tile whose FP32 sums fit the registers of eight warps, and the fewest bytes loaded for
 //   the work. 128-column MMAs read the activation rows twice from shared memory (238 us where this takes 216).
 //
-// What bounds it: with few rows a group, DRAM (gate/up of the DeepSeek-V3 shape: 8 experts, one row each, 43 us,
-// 5.5 TB/s; 256 experts, 6 rows each, 928 us, 8.0 TB/s). With many, the accumulate warps, about 735 clocks of
-// waits, tensor-memory loads and multiply-adds a K block alone and 950 beside the loads, against 512 of MMA (16 experts x
-// 512 rows: gate/up 204 us, 2360 TFLOP/s; down 119 us, 2020 TFLOP/s), and under sustained load the power limit.
+// What bounds it: with few rows a group, DRAM (gate/up of the DeepSeek-V3 shape: 8 experts, one row each, 44 us,
+// 5.3 TB/s; 226 experts, 7 rows each, 945-975 us, 6.8-7.0 TB/s, the copy rate). With many, the accumulate warps, about 735
+// clocks of waits, tensor-memory loads and multiply-adds a K block alone and 950 beside the loads, against 512 of MMA (16
+// experts x 512 rows: gate/up 208 us, 2310 TFLOP/s; down 119 us, 2025 TFLOP/s), tiles that a group does not fill (256
+// experts x 512 rows on average hold 1.12 times their rows: gate/up 1920 TFLOP/s of rows; 256 on average 1.25: down 1390),
+// and under sustained load the power limit (the 16 experts again and again: 225 and 128 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -10,7 +10,7 @@
 // read once, into registers as the BF16 values z are (16 registers a thread: four
 // chunks of eight values), by the fewest warps that hold it so; a block's amax takes
 // shuffles over its 16 (4) threads. 16384 x 7168 with residual and BF16 norm: 156 us,
-// 6.8 TB/s, the rate of a plain copy; one row: about 3 us, its latency.
+// 6.8 TB/s, the rate of a plain copy; one row: about 4 us, its latency.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 

@@ -8,8 +8,10 @@
 // for its run and counts its routes per expert in shared memory; the CTAs publish their counts, meet once (bounded
 // wait), and each derives the expert starts and its own places from all counts. So every route has its place without
 // an atomic whose order could show.
-// Bound by instruction issue on long prompts (a token's keys, and the choice among them: 16384 tokens of 256 experts
-// 22 us) and by latency on short ones (one token 4.5 us, 1533 tokens of 896 experts 21 us; 2 us more outside a graph).
+// What bounds it: 16384 tokens of 256 experts, 24 us: of a CTA's 43,000 clocks the picks take 27,100 (three or four
+// tokens a warp, one after another), the sums over all CTAs' counts 6,600, the meeting 4,300, the places 3,000; issue slots
+// are half used, and the largest stall is the CTA barrier. 1533 tokens of 896 experts, 23 us (96 CTAs, 39,800 clocks):
+// picks 19,100, sums 8,500, meeting 8,300. One token 6 us: latency.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
