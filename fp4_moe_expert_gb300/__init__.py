@@ -157,10 +157,12 @@ def kept_workspace_error(device=None):
     """Device error bits (Workspace.error, or-ed; 0 = none) of the workspaces kept for calls that were given none, on
     `device` (default: the current one). Synchronises the device. A workspace with an error is cleared, so that later
     calls are right again; what the calls since the error returned is not."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
     torch.cuda.synchronize(index)
     bits = 0
-    for key, ws in _ws_cache.items():
+    for key, ws in list(_ws_cache.items()):
         if key[0] == index:
             code = ws.error()
             if code != 0:
