@@ -56,6 +56,13 @@ SIGNATURES = {
     "fme_moe_route": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp, _vp, _vp,
                                _c_size, _vp]),
     "fme_moe_route_workspace": (_c_size, [_c_int] * 3),
+    "fme_moe_route_groups": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                      _c_float, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "fme_block_norm": (_c_int, [_vp, _c_ll, _vp, _c_int, _vp, _vp, _vp, _c_ll, _vp, _c_ll, _c_float, _vp, _c_int,
+                                _c_int, _c_float, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
+    "fme_linear_bf16": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _c_int, _vp, _c_ll, _c_int, _c_int, _c_int, _vp, _c_int,
+                                 _c_ll, _vp, _c_size, _vp]),
+    "fme_linear_bf16_workspace": (_c_size, [_c_int] * 3),
     "fme_moe_grouped_swiglu_fp8": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                             _c_float, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
     "fme_moe_grouped_gemm_fp8": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
@@ -504,6 +511,165 @@ def moe_route(logits, bias, top_k, scale=1.0, ids=None, weights=None, offsets=No
                              weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), tokens.data_ptr(),
                              ws.buf.data_ptr(), ws.nbytes, _launch_stream(dev)))
     return ids, weights, offsets, rows, tokens
+
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def moe_route_groups(logits, bias, top_k, score="sigmoid", groups=1, top_groups=None, group_top=None, renormalise=True,
+                     scale=1.0, ids=None, weights=None, offsets=None, rows=None, tokens=None, workspace=None):
+    """moe_route with other scores and with the experts limited to groups (fme_moe_route_groups): score "sigmoid" or
+    "softmax", bias [E] float32 or None, the experts of each token's top_groups (default: all) best of `groups` equal
+    runs, a group counting as the sum of its best group_top (1 or 2; default 2 where a group has as many) keys, weights
+    divided by their sum or (renormalise=False) not. Returns what moe_route returns; it takes moe_route's workspace."""
+    T, E = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be float32 or bfloat16")
+    if score not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
+    top_groups = groups if top_groups is None else top_groups
+    group_top = (2 if E >= 2 * groups else 1) if group_top is None else group_top
+    _need(logits, logits.dtype, (T, E), "logits")
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias", dev)
+    ids = _out(ids, (T, top_k), torch.int32, dev, "ids")
+    weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
+    offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets")
+    rows = _out(rows, (T * top_k,), torch.int32, dev, "rows")
+    tokens = _out(tokens, (T * top_k,), torch.int32, dev, "tokens")
+    if T == 0:
+        return ids, weights, offsets.zero_(), rows, tokens
+    ws = _stream_workspace(moe_route_workspace(T, E, top_k), dev, workspace)
+    ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
+    _check(lib.fme_moe_route_groups(logits.data_ptr(), ldt, _addr(bias), T, E, top_k, _SCORES[score], groups, top_groups,
+                                    group_top, int(bool(renormalise)), scale, ids.data_ptr(), weights.data_ptr(),
+                                    offsets.data_ptr(), rows.data_ptr(), tokens.data_ptr(), ws.buf.data_ptr(), ws.nbytes,
+                                    _launch_stream(dev)))
+    return ids, weights, offsets, rows, tokens
+
+
+_QUANT = {None: 0, "fp8": 1, "mxfp8": 2}
+
+
+def block_norm(x, gamma, residual=None, route_weights=None, shared_out=None, post_gamma=None, gate=None,
+               residual_scale=1.0, eps=1e-5, quant=None, ue8m0=False, want_normed=False, q=None, scales=None, normed=None,
+               residual_out=None):
+    """What stands between a block and the next (fme_block_norm): h = residual_scale * residual + gate * p with p = x or
+    (post_gamma [H]) its RMSNorm times post_gamma, then RMSNorm(h) * gamma and its quantisation.
+
+    x [T, H] BF16 (any row stride), or with route_weights [T, top_k] float32 the routes' rows [T * top_k, H], combined
+    as moe_finalize does (shared_out [T, H] added); gate BF16 [H] or [T, H], gamma [H] or None (no second norm), quant
+    None, "fp8" or "mxfp8". Returns (q, scales, residual_out, normed) as add_rmsnorm_fp8 / add_rmsnorm_mxfp8, q and
+    scales None without quant, normed None unless wanted (or given); residual_out [T, H] BF16 is h, and may be a dense
+    residual."""
+    ldx, dev = _rows(x, "x"), x.device
+    n, H = x.shape
+    T, top_k = n, 0
+    if quant not in _QUANT:
+        raise ValueError(f"quant: expected one of {list(_QUANT)}, got {quant!r}")
+    if route_weights is not None:
+        T, top_k = route_weights.shape
+        _need(route_weights, torch.float32, (T, top_k), "route_weights", dev)
+        if top_k == 0 or n != T * top_k:
+            raise ValueError(f"x: expected {T} * {top_k} rows, got {n}")
+    if shared_out is not None:
+        if route_weights is None:
+            raise ValueError("shared_out without route_weights")
+        _need(shared_out, torch.bfloat16, (T, H), "shared_out", dev)
+    for v, name in ((gamma, "gamma"), (post_gamma, "post_gamma")):
+        if v is not None:
+            _need(v, torch.bfloat16, (H,), name, dev)
+    ldg = ldr = 0
+    if gate is not None:
+        if gate.device != dev:
+            raise ValueError(f"gate: on {gate.device}, the other operands on {dev}")
+        if gate.dim() == 1:
+            _need(gate, torch.bfloat16, (H,), "gate", dev)
+        else:
+            ldg = _rows(gate, "gate")
+            if gate.shape != (T, H):
+                raise ValueError(f"gate: expected {(H,)} or {(T, H)}, got {tuple(gate.shape)}")
+    if residual is not None:
+        ldr = _rows(residual, "residual")
+        if residual.shape != (T, H):
+            raise ValueError(f"residual: expected {(T, H)}, got {tuple(residual.shape)}")
+        if residual.device != dev:
+            raise ValueError(f"residual: on {residual.device}, the other operands on {dev}")
+    if gamma is None and (quant is not None or want_normed or normed is not None):
+        raise ValueError("normed or quantised outputs without gamma")
+    if quant is None and (q is not None or scales is not None):
+        raise ValueError("q or scales without quant")
+    residual_out = _out(residual_out, (T, H), torch.bfloat16, dev, "residual_out")
+    if quant is not None:
+        mx = quant == "mxfp8"
+        q = _out(q, (T, H), torch.uint8, dev, "q")
+        scales = _out(scales, (T, H // (32 if mx else 128)), torch.uint8 if mx else torch.float32, dev, "scales")
+    if want_normed or normed is not None:
+        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+    if T == 0:
+        return q, scales, residual_out, normed
+    _check(lib.fme_block_norm(x.data_ptr(), ldx, _addr(route_weights), top_k, _addr(shared_out), _addr(post_gamma),
+                              _addr(gate), ldg, _addr(residual), ldr, residual_scale, _addr(gamma), T, H, eps,
+                              _QUANT[quant], int(bool(ue8m0)), _addr(q), _addr(scales), _addr(normed),
+                              residual_out.data_ptr(), _launch_stream(dev)))
+    return q, scales, residual_out, normed
+
+
+_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
+
+
+def linear_bf16_workspace(M, N, K):
+    return lib.fme_linear_bf16_workspace(M, N, K)
+
+
+def _stride(t, dtype, name, align=1):
+    """Row stride of a CUDA matrix with contiguous rows; one row's, which nothing steps by, rounded up to `align`."""
+    if t.dtype != dtype or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a CUDA {dtype} matrix with contiguous rows, got {t.dtype} {tuple(t.shape)} "
+                         f"strides={t.stride()} cuda={t.is_cuda}")
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // align) * align
+
+
+def linear_bf16(x, w, bias=None, activation=None, residual=None, out_dtype=None, out=None, workspace=None):
+    """act(x w^T + bias) + residual (fme_linear_bf16): x [M, K] and w [N, K] BF16 whose rows start at multiples of 16
+    bytes, bias [N] float32, activation None, "relu", "silu", "gelu" or "sigmoid", residual [M, N] of the output's type.
+    Returns out [M, N] of out_dtype (BF16 unless float32 is asked for), or the given out, whose rows may be strided and
+    which may be residual."""
+    ldx, ldw, dev = _stride(x, torch.bfloat16, "x", 8), _stride(w, torch.bfloat16, "w", 8), x.device
+    M, K = x.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w: expected {K} columns, got {w.shape[1]}")
+    if w.device != dev:
+        raise ValueError(f"w: on {w.device}, the other operands on {dev}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {list(_ACTIVATIONS)}, got {activation!r}")
+    if bias is not None:
+        _need(bias, torch.float32, (N,), "bias", dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    ldo, ldr = N, 0
+    if residual is not None:
+        ldr = _stride(residual, out_dtype, "residual")
+    if out is not None:
+        ldo = _stride(out, out_dtype, "out")
+    for t, name in ((out, "out"), (residual, "residual")):
+        if t is not None and t.shape != (M, N):
+            raise ValueError(f"{name}: expected {(M, N)}, got {tuple(t.shape)}")
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the other operands on {dev}")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    if M == 0:
+        return out
+    ws = _stream_workspace(linear_bf16_workspace(M, N, K), dev, workspace)
+    _check(lib.fme_linear_bf16(x.data_ptr(), ldx, w.data_ptr(), ldw, _addr(bias), _ACTIVATIONS[activation],
+                               _addr(residual), ldr, M, N, K, out.data_ptr(), int(out_dtype == torch.bfloat16), ldo,
+                               ws.buf.data_ptr(), ws.nbytes, _launch_stream(dev)))
+    return out
 
 
 def moe_grouped_fp8_workspace(R, K, N, E):

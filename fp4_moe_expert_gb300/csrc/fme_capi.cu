@@ -501,6 +501,8 @@ int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, lo
                            static_cast<cudaStream_t>(stream));
 }
 
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
 static int check_route_shapes(int T, int E, int top_k) {
   FME_REQUIRE(T >= 0 && T <= (1 << 20), FME_EINVAL, "T=%d outside [0, 2^20]", T);
   FME_REQUIRE(E >= 1 && E <= kMaxExperts, FME_EUNSUPPORTED, "E=%d outside [1, %d]", E, kMaxExperts);
@@ -525,8 +527,181 @@ int fme_moe_route(const void* logits, int logits_dtype, const float* bias, int T
   FME_REQUIRE(!misaligned(logits) && !misaligned(bias) && !misaligned(ids) && !misaligned(weights) &&
                   !misaligned(offsets) && !misaligned(rows) && !misaligned(tokens) && !misaligned(workspace),
               FME_EALIGN, "every pointer must be 16-byte aligned");
-  return route(logits, logits_dtype, bias, T, E, top_k, scale, ids, weights, offsets, rows, tokens, workspace,
+  return route(logits, logits_dtype, bias, T, E, top_k, nullptr, scale, ids, weights, offsets, rows, tokens, workspace,
                workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int fme_moe_route_groups(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, int score,
+                         int groups, int top_groups, int group_top, int renormalise, float scale, int32_t* ids,
+                         float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  FME_REQUIRE(logits && ids && weights && offsets && rows && tokens, FME_EINVAL, "null pointer argument");
+  const int st = check_route_shapes(T, E, top_k);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(logits_dtype == FME_F32 || logits_dtype == FME_BF16, FME_EINVAL, "logits_dtype=%d", logits_dtype);
+  FME_REQUIRE(score == FME_SIGMOID || score == FME_SOFTMAX, FME_EINVAL, "score=%d", score);
+  FME_REQUIRE(groups >= 1 && groups <= 32 && E % groups == 0, FME_EINVAL, "groups=%d must be a divisor of E=%d up to 32",
+              groups, E);
+  FME_REQUIRE(top_groups >= 1 && top_groups <= groups && top_k <= top_groups * (E / groups), FME_EINVAL,
+              "top_groups=%d outside [1, groups=%d], or too few for top_k=%d of %d experts each", top_groups, groups, top_k,
+              E / groups);
+  FME_REQUIRE((group_top == 1 || group_top == 2) && group_top <= E / groups, FME_EINVAL,
+              "group_top=%d must be 1 or 2 and at most the %d experts of a group", group_top, E / groups);
+  FME_REQUIRE(std::isfinite(scale), FME_EINVAL, "scale must be finite");
+  FME_REQUIRE(!misaligned(logits) && !misaligned(bias) && !misaligned(ids) && !misaligned(weights) &&
+                  !misaligned(offsets) && !misaligned(rows) && !misaligned(tokens) && !misaligned(workspace),
+              FME_EALIGN, "every pointer must be 16-byte aligned");
+  RouteScores s;
+  s.softmax = score == FME_SOFTMAX;
+  s.renormalise = renormalise != 0;
+  s.groups = groups;
+  s.top_groups = top_groups;
+  s.group_top = group_top;
+  return route(logits, logits_dtype, bias, T, E, top_k, &s, scale, ids, weights, offsets, rows, tokens, workspace,
+               workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+// A tensor's bytes, for the refusal of outputs that overlap other operands: rows of `row` bytes, `pitch` apart.
+struct Span {
+  uintptr_t at = 0;
+  unsigned long long bytes = 0, pitch = 0, row = 0;
+  Span(const void* p, long long rows, long long pitch_, long long row_) {
+    if (p == nullptr || rows <= 0) return;
+    at = reinterpret_cast<uintptr_t>(p);
+    pitch = pitch_;
+    row = row_;
+    bytes = static_cast<unsigned long long>(rows - 1) * pitch + row;
+  }
+  bool meets(const Span& o) const {
+    if (bytes == 0 || o.bytes == 0 || at >= o.at + o.bytes || o.at >= at + bytes) return false;
+    if (pitch != o.pitch || bytes == row || o.bytes == o.row) return true;
+    // Rows of one wider buffer: where this one's start within the other's.
+    const unsigned long long d = at >= o.at ? (at - o.at) % pitch : (pitch - (o.at - at) % pitch) % pitch;
+    return d < o.row || d + row > pitch;
+  }
+};
+}  // namespace
+
+int fme_block_norm(const void* x, long long ldx, const float* route_weights, int top_k, const void* shared_out,
+                   const void* post_gamma, const void* gate, long long ldg, const void* residual, long long ldr,
+                   float residual_scale, const void* gamma, int T, int H, float eps, int quant, int ue8m0, uint8_t* q,
+                   void* scales, void* normed, void* residual_out, void* stream) {
+  FME_REQUIRE(quant >= FME_QUANT_NONE && quant <= FME_QUANT_MXFP8, FME_EINVAL, "quant=%d", quant);
+  FME_REQUIRE(x && residual_out, FME_EINVAL, "null pointer argument");
+  FME_REQUIRE((quant != FME_QUANT_NONE) == (q != nullptr) && (q != nullptr) == (scales != nullptr), FME_EINVAL,
+              "q and scales come with quant, and only with it");
+  FME_REQUIRE(gamma != nullptr || (q == nullptr && normed == nullptr), FME_EINVAL, "normed or q without gamma");
+  FME_REQUIRE(top_k >= 0 && top_k <= kMaxTopK && (top_k > 0) == (route_weights != nullptr) &&
+                  (top_k > 0 || shared_out == nullptr),
+              FME_EINVAL, "top_k=%d outside [0, %d], or route_weights or shared_out at odds with it", top_k, kMaxTopK);
+  const long long routes = static_cast<long long>(T) * (top_k > 0 ? top_k : 1);
+  FME_REQUIRE(T >= 0 && T <= (1 << 20) && routes <= (1 << 25), FME_EINVAL, "T=%d outside [0, 2^20], or above 2^25 rows", T);
+  const int block = quant == FME_QUANT_FP8 ? 128 : quant == FME_QUANT_MXFP8 ? 32 : 8;
+  FME_REQUIRE(H >= block && H % block == 0 && H <= 16384, FME_EINVAL, "H=%d must be a multiple of %d in [%d, 16384]", H,
+              block, block);
+  FME_REQUIRE(ldx >= H && ldx % 8 == 0 && (residual == nullptr || (ldr >= H && ldr % 8 == 0)) &&
+                  (gate == nullptr || ldg == 0 || (ldg >= H && ldg % 8 == 0)),
+              FME_EINVAL, "row strides ldx=%lld, ldr=%lld, ldg=%lld must be multiples of 8 and at least H=%d (ldg: or 0)",
+              ldx, ldr, ldg, H);
+  FME_REQUIRE(ldx <= (1LL << 34) && (residual == nullptr || ldr <= (1LL << 34)) && (gate == nullptr || ldg <= (1LL << 34)),
+              FME_EINVAL, "row stride above 2^34");
+  FME_REQUIRE(std::isfinite(residual_scale), FME_EINVAL, "residual_scale must be finite");
+  FME_REQUIRE(eps >= 0.0f && std::isfinite(eps), FME_EINVAL, "eps must be finite and >= 0");
+  FME_REQUIRE(!misaligned(x) && !misaligned(shared_out) && !misaligned(post_gamma) && !misaligned(gate) &&
+                  !misaligned(residual) && !misaligned(gamma) && !misaligned(q) && !misaligned(normed) &&
+                  !misaligned(residual_out) && (quant != FME_QUANT_FP8 || !misaligned(scales)) &&
+                  !misaligned4(route_weights),
+              FME_EALIGN, "every pointer must be 16-byte aligned (route_weights 4-byte, MXFP8 scales any)");
+  const Span in[] = {{x, routes, 2 * ldx, 2LL * H},          {route_weights, T, 4LL * top_k, 4LL * top_k},
+                     {shared_out, T, 2LL * H, 2LL * H},      {post_gamma, 1, 0, 2LL * H},
+                     {gate, ldg == 0 ? 1 : T, 2 * ldg, 2LL * H}, {gamma, 1, 0, 2LL * H},
+                     {residual, T, 2 * ldr, 2LL * H}};
+  const long long per_row = quant == FME_QUANT_FP8 ? H / 32 : quant == FME_QUANT_MXFP8 ? H / 32 : 0;
+  const Span out[] = {{residual_out, T, 2LL * H, 2LL * H}, {normed, T, 2LL * H, 2LL * H}, {q, T, H, H},
+                      {scales, T, per_row, per_row}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 7; ++j)
+      FME_REQUIRE(!out[i].meets(in[j]) || (i == 0 && j == 6 && residual_out == residual && ldr == H), FME_EINVAL,
+                  "an output overlaps an input (residual_out may be a residual of dense rows)");
+    for (int j = 0; j < i; ++j) FME_REQUIRE(!out[i].meets(out[j]), FME_EINVAL, "two outputs overlap");
+  }
+  if (T == 0) return FME_OK;
+  BlockNorm b;
+  b.x = x;
+  b.ldx = ldx;
+  b.route_weights = route_weights;
+  b.top_k = top_k;
+  b.shared_out = shared_out;
+  b.post_gamma = post_gamma;
+  b.gate = gate;
+  b.ldg = ldg;
+  b.residual = residual;
+  b.ldr = ldr;
+  b.residual_scale = residual_scale;
+  b.gamma = gamma;
+  b.T = T;
+  b.H = H;
+  b.eps = eps;
+  b.quant = quant;
+  b.ue8m0 = ue8m0;
+  b.q = q;
+  b.scales = scales;
+  b.normed = normed;
+  b.residual_out = residual_out;
+  return block_norm(b, static_cast<cudaStream_t>(stream));
+}
+
+static int check_linear_shapes(int M, int N, int K) {
+  FME_REQUIRE(M >= 0 && M <= (1 << 20), FME_EINVAL, "M=%d outside [0, 2^20]", M);
+  FME_REQUIRE(N >= 1 && N <= (1 << 17) && K >= 1 && K <= (1 << 17), FME_EINVAL, "N=%d or K=%d outside [1, 2^17]", N, K);
+  return FME_OK;
+}
+
+size_t fme_linear_bf16_workspace(int M, int N, int K) {
+  if (check_linear_shapes(M, N, K) != FME_OK) return 0;
+  return linear_workspace_bytes(M, N, K);
+}
+
+int fme_linear_bf16(const void* x, long long ldx, const void* w, long long ldw, const float* bias, int activation,
+                    const void* residual, long long ldr, int M, int N, int K, void* out, int out_dtype, long long ldo,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  FME_REQUIRE(x && w && out, FME_EINVAL, "null pointer argument");
+  const int st = check_linear_shapes(M, N, K);
+  if (st != FME_OK) return st;
+  FME_REQUIRE(ldx >= K && ldx % 8 == 0 && ldw >= K && ldw % 8 == 0, FME_EINVAL,
+              "row strides ldx=%lld and ldw=%lld must be multiples of 8 and at least K=%d", ldx, ldw, K);
+  FME_REQUIRE(ldx <= (1LL << 34) && ldw <= (1LL << 34) && ldo <= (1LL << 34) &&
+                  (residual == nullptr || ldr <= (1LL << 34)),
+              FME_EINVAL, "row stride above 2^34");
+  FME_REQUIRE(ldo >= N && (residual == nullptr || ldr >= N), FME_EINVAL,
+              "row strides ldo=%lld and ldr=%lld must be at least N=%d", ldo, ldr, N);
+  FME_REQUIRE(activation >= FME_ACT_NONE && activation <= FME_ACT_SIGMOID, FME_EINVAL, "activation=%d", activation);
+  FME_REQUIRE(out_dtype == FME_F32 || out_dtype == FME_BF16, FME_EINVAL, "out_dtype=%d", out_dtype);
+  const long long size = out_dtype == FME_F32 ? 4 : 2;
+  FME_REQUIRE(!misaligned(x) && !misaligned(w) && !misaligned4(bias) && !misaligned(workspace) &&
+                  reinterpret_cast<uintptr_t>(out) % size == 0 && reinterpret_cast<uintptr_t>(residual) % size == 0,
+              FME_EALIGN, "x, w and the workspace must be 16-byte aligned, the others to their element");
+  const Span o(out, M, size * ldo, size * N), r(residual, M, size * ldr, size * N);
+  FME_REQUIRE(!o.meets(Span(x, M, 2 * ldx, 2LL * K)) && !o.meets(Span(w, N, 2 * ldw, 2LL * K)) &&
+                  !o.meets(Span(bias, 1, 0, 4LL * N)) && (!o.meets(r) || (out == residual && ldo == ldr)),
+              FME_EINVAL, "out overlaps an input (it may be residual, with the same row stride)");
+  Linear l;
+  l.x = x;
+  l.ldx = ldx;
+  l.w = w;
+  l.ldw = ldw;
+  l.bias = bias;
+  l.act = activation;
+  l.residual = residual;
+  l.ldr = ldr;
+  l.M = M;
+  l.N = N;
+  l.K = K;
+  l.out = out;
+  l.out_f32 = out_dtype == FME_F32;
+  l.ldo = ldo;
+  return linear(l, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 static int check_grouped_shapes(int R, int K, int N, int E) {
@@ -542,8 +717,6 @@ size_t fme_moe_grouped_fp8_workspace(int R, int K, int N, int E) {
   if (check_grouped_shapes(R, K, N, E) != FME_OK) return 0;
   return grouped_fp8_workspace_bytes();
 }
-
-static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 int fme_moe_grouped_swiglu_fp8(const uint8_t* a, const float* sa, int a_rows, const uint8_t* w13, const float* s13,
                                const int32_t* offsets, const int32_t* in_rows, int R, int H, int I, int E, float limit,

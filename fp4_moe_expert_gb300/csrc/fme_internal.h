@@ -90,11 +90,59 @@ int add_rmsnorm_quant(const void* x, long long ldx, const void* residual, long l
                       float eps, int ue8m0, uint8_t* q, float* scales, uint8_t* mxscales, void* normed,
                       void* residual_out, cudaStream_t st);
 
-// Picks and weights of T tokens and their routes sorted by expert (arguments validated).
+// How fme_moe_route_groups scores and limits the experts.
+struct RouteScores {
+  bool softmax = false, renormalise = true;
+  int groups = 1, top_groups = 1, group_top = 1;
+};
+// Picks and weights of T tokens and their routes sorted by expert (arguments validated). Without `scored`:
+// fme_moe_route's rule.
 size_t route_workspace_bytes(int T, int E);
-int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale, int32_t* ids,
-          float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace, size_t workspace_bytes,
-          cudaStream_t st);
+int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, const RouteScores* scored,
+          float scale, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+          size_t workspace_bytes, cudaStream_t st);
+
+// What stands between a block and the next (arguments validated; null pointers: left out).
+struct BlockNorm {
+  const void* x = nullptr;
+  long long ldx = 0;
+  const float* route_weights = nullptr;
+  int top_k = 0;
+  const void* shared_out = nullptr;
+  const void* post_gamma = nullptr;
+  const void* gate = nullptr;
+  long long ldg = 0;
+  const void* residual = nullptr;
+  long long ldr = 0;
+  float residual_scale = 1.0f;
+  const void* gamma = nullptr;
+  int T = 0, H = 0;
+  float eps = 0.0f;
+  int quant = 0, ue8m0 = 0;
+  uint8_t* q = nullptr;
+  void* scales = nullptr;
+  void* normed = nullptr;
+  void* residual_out = nullptr;
+};
+int block_norm(const BlockNorm& b, cudaStream_t st);
+
+// act(x w^T + bias) + residual (arguments validated).
+struct Linear {
+  const void* x = nullptr;
+  long long ldx = 0;
+  const void* w = nullptr;
+  long long ldw = 0;
+  const float* bias = nullptr;
+  int act = 0;
+  const void* residual = nullptr;
+  long long ldr = 0;
+  int M = 0, N = 0, K = 0;
+  void* out = nullptr;
+  int out_f32 = 0;
+  long long ldo = 0;
+};
+size_t linear_workspace_bytes(int M, int N, int K);
+int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_t st);
 
 // A product grouped by expert (arguments validated): with q the SwiGLU
 // epilogue (N = 2I, q / sq written at the grouped row), else BF16 rows.

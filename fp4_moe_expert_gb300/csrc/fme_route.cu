@@ -8,6 +8,11 @@
 // for its run and counts its routes per expert in shared memory; the CTAs publish their counts, meet once (bounded
 // wait), and each derives the expert starts and its own places from all counts. So every route has its place without
 // an atomic whose order could show.
+// The scored form (SCORED, fme_moe_route_groups) differs in the picks alone: sigmoid or softmax scores p, keys p + bias or, without
+// a bias, the logits themselves (their order is the scores', and neither saturates nor underflows); the experts of the
+// groups whose best one or two keys sum to less than those of the top_groups best groups are out; weights p / (sum of the
+// picked p) * scale or p * scale. A softmax row's picks are weighed by exp(l - max): the sum over the row cancels.
+//
 // What bounds it: 16384 tokens of 256 experts, 24 us: of a CTA's 43,000 clocks the picks take 27,100 (three or four
 // tokens a warp, one after another), the sums over all CTAs' counts 6,600, the meeting 4,300, the places 3,000; issue slots
 // are half used, and the largest stall is the CTA barrier. 1533 tokens of 896 experts, 23 us (96 CTAs, 39,800 clocks):
@@ -29,9 +34,10 @@ __host__ __device__ constexpr int rt_warps() { return J <= 8 ? 32 : 16; }
 
 struct RtArgs {
   const void* logits;
-  const float* bias;
+  const float* bias;  // scored form: may be null
   int logits_f32, vec, T, E, top_k;
   float scale;
+  int softmax, groups, group_size, top_groups, group_top, renormalise;  // scored form
   int per_cta, per_warp;  // tokens
   int pitch;              // experts in a row of counts: E rounded up to 8
   int32_t* ids;
@@ -102,23 +108,15 @@ __device__ __forceinline__ V rt_sort(V v, int lane) {
   return v;
 }
 
-// The picks of token t: lane r < top_k gets rank r's expert and weight. `cand`: 32 words of this warp's.
+// The expert of rank `lane` (lanes below top_k) among the keys ky of experts J * lane ..; key 0: no expert. At least top_k keys
+// are not 0. `cand`: 32 words of this warp's.
 //
-// The top_k-th largest of the 32 lane maxima is at most the top_k-th largest key. The keys from it up are few (about
-// 9 of 256 for 8 picks, 22 of 896 for 16): they move to one a lane and are sorted, key first, lower expert first.
+// The top_k-th largest of the 32 lane maxima (`best`) is at most the top_k-th largest key. The keys from it up are few
+// (about 9 of 256 for 8 picks, 22 of 896 for 16): they move to one a lane and are sorted, key first, lower expert first.
 // Where they are more than 32, the picks are taken one after another instead.
 template <int J>
-__device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J], const float (&l)[J], int t, int lane,
-                                        unsigned long long* cand, int& my_e, float& my_w) {
-  uint32_t ky[J];
-  uint32_t best = 0u;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    // At least 1, so that an expert (a NaN key, too) always stands above a lane's empty places.
-    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(__fadd_rn(rt_sigmoid(l[j]), bias[j]))) : 0u;
-    best = max(best, ky[j]);
-  }
-  const uint32_t floor_key = max(1u, __shfl_sync(0xFFFFFFFFu, rt_sort(best, lane), a.top_k - 1));
+__device__ __forceinline__ int rt_select(int top_k, uint32_t (&ky)[J], uint32_t best, int lane, unsigned long long* cand) {
+  const uint32_t floor_key = max(1u, __shfl_sync(0xFFFFFFFFu, rt_sort(best, lane), top_k - 1));
   int count = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -138,7 +136,7 @@ __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J],
   } else {
     mine = 0;
 #pragma unroll 1
-    for (int r = 0; r < a.top_k; ++r) {
+    for (int r = 0; r < top_k; ++r) {
       uint32_t top = 0u;
       int top_j = 0;
 #pragma unroll
@@ -156,6 +154,22 @@ __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J],
         if (lane == win && j == top_j) ky[j] = 0u;
     }
   }
+  return mine;
+}
+
+// The picks of token t: lane r < top_k gets rank r's expert and weight.
+template <int J>
+__device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J], const float (&l)[J], int t, int lane,
+                                        unsigned long long* cand, int& my_e, float& my_w) {
+  uint32_t ky[J];
+  uint32_t best = 0u;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    // At least 1, so that an expert (a NaN key, too) always stands above a lane's empty places.
+    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(__fadd_rn(rt_sigmoid(l[j]), bias[j]))) : 0u;
+    best = max(best, ky[j]);
+  }
+  const int mine = rt_select<J>(a.top_k, ky, best, lane, cand);
   const float s =
       lane < a.top_k ? rt_sigmoid(rt_value(a.logits, a.logits_f32, static_cast<size_t>(t) * a.E + mine)) : 0.0f;
   float total = 0.0f;
@@ -164,7 +178,115 @@ __device__ __forceinline__ void rt_pick(const RtArgs& a, const float (&bias)[J],
   my_w = __fmul_rn(__fdiv_rn(s, total), a.scale);
 }
 
+// The float of an ordered key.
+__device__ __forceinline__ float rt_from_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Bit g: group g is among the top_groups whose best group_top keys sum to the most (ties: lower group). gk: keys of what the
+// groups are compared by, 0 past the last expert; a group has group_top experts at least.
 template <int J>
+__device__ __forceinline__ uint32_t rt_groups(const RtArgs& a, const uint32_t (&gk)[J], int lane) {
+  uint32_t mine = 0u;  // lane g: group g's sum, as a key
+#pragma unroll 1
+  for (int g = 0; g < a.groups; ++g) {
+    const int lo = g * a.group_size, hi = lo + a.group_size;
+    uint32_t first = 0u, second = 0u;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t k = J * lane + j >= lo && J * lane + j < hi ? gk[j] : 0u;
+      second = max(second, min(first, k));
+      first = max(first, k);
+    }
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, first);
+    uint32_t sum = top;
+    if (a.group_top == 2) {
+      const int win = __ffs(__ballot_sync(0xFFFFFFFFu, first == top)) - 1;
+      const uint32_t next = __reduce_max_sync(0xFFFFFFFFu, lane == win ? second : first);
+      sum = max(1u, ordered_key(__fadd_rn(rt_from_key(top), rt_from_key(next))));
+    }
+    if (lane == g) mine = sum;
+  }
+  int rank = 0;
+#pragma unroll 1
+  for (int g = 0; g < a.groups; ++g) {
+    const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine, g);
+    rank += k > mine || (k == mine && g < lane);
+  }
+  return __ballot_sync(0xFFFFFFFFu, lane < a.groups && rank < a.top_groups);
+}
+
+// rt_pick of the scored form.
+template <int J>
+__device__ __forceinline__ void rt_pick_scored(const RtArgs& a, const float (&bias)[J], const float (&l)[J], int t, int lane,
+                                               unsigned long long* cand, int& my_e, float& my_w) {
+  float m = 0.0f, inv = 1.0f;  // softmax: scores are exp(l - m) * inv
+  float p[J];
+  if (a.softmax) {
+    m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (J * lane + j < a.E) m = fmaxf(m, l[j]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (m == -INFINITY) m = 0.0f;  // nothing but -inf: every score is 0
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      p[j] = J * lane + j < a.E ? expf(__fsub_rn(l[j], m)) : 0.0f;
+      sum = __fadd_rn(sum, p[j]);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
+    inv = sum == 0.0f ? 0.0f : recip_rn(sum);  // sum in [1, 1024], or 0 (or NaN)
+#pragma unroll
+    for (int j = 0; j < J; ++j) p[j] = __fmul_rn(p[j], inv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) p[j] = rt_sigmoid(l[j]);
+  }
+  uint32_t ky[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (a.bias != nullptr) p[j] = __fadd_rn(p[j], bias[j]);
+    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(a.bias != nullptr ? p[j] : l[j])) : 0u;
+  }
+  if (a.top_groups < a.groups) {
+    uint32_t gk[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      gk[j] = a.bias != nullptr || a.group_top == 1 || ky[j] == 0u ? ky[j] : max(1u, ordered_key(p[j]));
+    const uint32_t open = rt_groups<J>(a, gk, lane);
+    int g = J * lane / a.group_size, next = (g + 1) * a.group_size;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (J * lane + j == next) {
+        ++g;
+        next += a.group_size;
+      }
+      if (g < 32 && !(open >> g & 1u)) ky[j] = 0u;
+    }
+  }
+  uint32_t best = 0u;
+#pragma unroll
+  for (int j = 0; j < J; ++j) best = max(best, ky[j]);
+  const int mine = rt_select<J>(a.top_k, ky, best, lane, cand);
+  float s = 0.0f;
+  if (lane < a.top_k) {
+    const float v = rt_value(a.logits, a.logits_f32, static_cast<size_t>(t) * a.E + mine);
+    s = a.softmax ? expf(__fsub_rn(v, m)) : rt_sigmoid(v);
+  }
+  my_e = mine;
+  if (a.renormalise) {
+    float total = 0.0f;
+    for (int r = 0; r < a.top_k; ++r) total = __fadd_rn(total, __shfl_sync(0xFFFFFFFFu, s, r));
+    my_w = total == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(s, total), a.scale);
+  } else {
+    my_w = __fmul_rn(a.softmax ? __fmul_rn(s, inv) : s, a.scale);
+  }
+}
+
+template <int J, bool SCORED>
 __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs a) {
   constexpr int kRtWarps = rt_warps<J>(), kRtThreads = 32 * kRtWarps;
   __shared__ uint16_t seen[kRtWarps][32 * J];    // routes of a warp's run per expert, then its next place
@@ -189,13 +311,16 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
 #pragma unroll
     for (int j = 0; j < J; ++j) bias[j] = l[j] = next[j] = 0.0f;
     rt_load<J>(a, a.logits, a.logits_f32, static_cast<size_t>(t0) * a.E, lane, l);
-    rt_load<J>(a, a.bias, true, 0, lane, bias);
+    if (!SCORED || a.bias != nullptr) rt_load<J>(a, a.bias, true, 0, lane, bias);
     __syncwarp();
     for (int t = t0; t < t1; ++t) {
       if (t + 1 < t1) rt_load<J>(a, a.logits, a.logits_f32, static_cast<size_t>(t + 1) * a.E, lane, next);
       int e;
       float w;
-      rt_pick<J>(a, bias, l, t, lane, u.cand[warp], e, w);
+      if (SCORED)
+        rt_pick_scored<J>(a, bias, l, t, lane, u.cand[warp], e, w);
+      else
+        rt_pick<J>(a, bias, l, t, lane, u.cand[warp], e, w);
       if (lane < a.top_k) {
         a.ids[static_cast<size_t>(t) * a.top_k + lane] = e;
         a.weights[static_cast<size_t>(t) * a.top_k + lane] = w;
@@ -324,9 +449,9 @@ size_t route_workspace_bytes(int T, int E) {
   return 256 + ((static_cast<size_t>(rt_ctas(T)) * rt_pitch(E) * sizeof(uint16_t) + 255) & ~size_t(255));
 }
 
-int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, float scale, int32_t* ids,
-          float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace, size_t workspace_bytes,
-          cudaStream_t st) {
+int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, const RouteScores* scored,
+          float scale, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+          size_t workspace_bytes, cudaStream_t st) {
   const size_t need = route_workspace_bytes(T, E);
   if (workspace == nullptr || workspace_bytes < need)
     return set_last_error(FME_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -348,6 +473,14 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   a.E = E;
   a.top_k = top_k;
   a.scale = scale;
+  if (scored != nullptr) {
+    a.softmax = scored->softmax ? 1 : 0;
+    a.groups = scored->groups;
+    a.group_size = E / scored->groups;
+    a.top_groups = scored->top_groups;
+    a.group_top = scored->group_top;
+    a.renormalise = scored->renormalise ? 1 : 0;
+  }
   // All CTAs of a launch meet, so there are no more than SMs.
   const int ctas = rt_ctas(T) < sms ? rt_ctas(T) : sms;
   a.per_cta = (T + ctas - 1) / ctas;
@@ -376,7 +509,17 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   attr[1].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  void (*kernel)(RtArgs) = E <= 64 ? route_kernel<2> : E <= 256 ? route_kernel<8> : E <= 512 ? route_kernel<16> : route_kernel<32>;
+  void (*kernel)(RtArgs);
+  if (scored != nullptr)
+    kernel = E <= 64    ? route_kernel<2, true>
+             : E <= 256 ? route_kernel<8, true>
+             : E <= 512 ? route_kernel<16, true>
+                        : route_kernel<32, true>;
+  else
+    kernel = E <= 64    ? route_kernel<2, false>
+             : E <= 256 ? route_kernel<8, false>
+             : E <= 512 ? route_kernel<16, false>
+                        : route_kernel<32, false>;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "route launch: %s", cudaGetErrorString(err));
   return FME_OK;

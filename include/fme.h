@@ -52,6 +52,15 @@ typedef enum {
 } fme_status;
 
 typedef enum { FME_F32 = 0, FME_BF16 = 1 } fme_dtype;
+typedef enum { FME_SIGMOID = 0, FME_SOFTMAX = 1 } fme_score;
+typedef enum { FME_QUANT_NONE = 0, FME_QUANT_FP8 = 1, FME_QUANT_MXFP8 = 2 } fme_quant;
+typedef enum {
+  FME_ACT_NONE = 0,
+  FME_ACT_RELU = 1,    /* max(z, 0) */
+  FME_ACT_SILU = 2,    /* z / (1 + exp(-z)) */
+  FME_ACT_GELU = 3,    /* z P(N(0, 1) < z) = z (1 + erf(z / sqrt 2)) / 2 */
+  FME_ACT_SIGMOID = 4  /* 1 / (1 + exp(-z)) */
+} fme_activation;
 
 /* One-line reason for the last non-OK status returned on this host thread. */
 const char* fme_last_error(void);
@@ -499,6 +508,98 @@ int fme_moe_grouped_gemm_fp8(const uint8_t* a, const float* sa, int a_rows, cons
 /* Workspace bytes the two grouped products need (N weight rows per expert: 2I
  * for the first; 0 on bad sizes). */
 size_t fme_moe_grouped_fp8_workspace(int R, int K, int N, int E);
+
+/*
+ * fme_moe_route with other scores and with the experts limited to groups.
+ *
+ * No counterpart in the pages. Per token, in FP32:
+ *   p = sigmoid(logits), or softmax over the E logits;  key = p + bias;
+ *   with top_groups < groups: the experts lie in `groups` equal runs of E /
+ *   groups; a group counts as the sum of its best group_top (1 or 2) keys, and
+ *   the experts outside the top_groups best groups are out (equal groups: the
+ *   lower one stays);
+ *   the top_k largest keys of the rest, in descending order (equal keys: the
+ *   lower expert first);
+ *   weights = p / (sum of the picked p) * scale with renormalise, else p *
+ *   scale.
+ * Without a bias (NULL) experts are picked by their logits, whose order is the
+ * scores', so that scores that saturate or underflow still differ; groups are
+ * compared by logits with group_top 1, by scores with 2.
+ * A score that underflows is 0, and a token whose picked scores are all 0 (a
+ * row of -inf logits) gets zero weights. A +inf or NaN logit makes softmax
+ * weights NaN; its picks are distinct, in range and in open groups all the
+ * same.
+ *
+ * Arguments, outputs, limits, workspace and errors as fme_moe_route, and: bias
+ *   may be NULL, score FME_SIGMOID or FME_SOFTMAX, groups in [1, 32] a divisor
+ *   of E, top_groups in [1, groups], group_top 1 or 2 and at most E / groups,
+ *   top_k <= top_groups * (E / groups).
+ */
+int fme_moe_route_groups(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, int score,
+                         int groups, int top_groups, int group_top, int renormalise, float scale, int32_t* ids,
+                         float* weights, int32_t* offsets, int32_t* rows, int32_t* tokens, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * What stands between a block and the next, in one pass (no counterpart in the
+ * pages). Per token t, in FP32:
+ *   o = x[t] with top_k = 0; else sum over r ascending of route_weights[t, r] *
+ *       x[t * top_k + r] (+ shared_out[t]), as fme_moe_finalize but not rounded;
+ *   p = o * rstd(o) * post_gamma, rstd(v) = 1 / sqrt(mean v^2 + eps) (p = o
+ *       without post_gamma);
+ *   h = residual_scale * residual[t] + gate * p (terms without their operand:
+ *       left out);
+ *   y = h * rstd(h) * gamma;
+ *   residual_out = bf16(h), normed = bf16(y), and with quant FME_QUANT_FP8 or
+ *   FME_QUANT_MXFP8 q and scales of y as fme_add_rmsnorm_fp8 / _mxfp8 write
+ *   them. The second norm takes the FP32 h, not its rounding.
+ *
+ * Arguments: x [T * max(top_k, 1), H] BF16 with row stride ldx; route_weights
+ *   [T, top_k] FP32 (with top_k > 0 only); shared_out [T, H] BF16 or NULL
+ *   (with top_k > 0 only); post_gamma [H] BF16 or NULL; gate BF16 or NULL, row
+ *   t at gate + t * ldg (ldg = 0: one row for every token); residual [T, H]
+ *   BF16 with row stride ldr, or NULL; gamma [H] BF16 or NULL (then there is no
+ *   second norm: quant is FME_QUANT_NONE and normed NULL). Outputs:
+ *   residual_out [T, H] BF16; normed [T, H] BF16 or NULL; q [T, H] E4M3 and
+ *   scales [T, H/128] FP32 or [T, H/32] bytes with quant, else NULL.
+ *   ue8m0: FP8 scales are rounded up to powers of two. 0 <= T <= 2^20; T *
+ *   max(top_k, 1) <= 2^25; H a multiple of 8 (FP8: 128, MXFP8: 32) up to 16384;
+ *   strides multiples of 8, at least H and at most 2^34; top_k in [0, 32]; residual_scale
+ *   finite; eps finite and >= 0. Pointers 16-byte aligned (route_weights
+ *   4-byte, MXFP8 scales any).
+ * residual_out may be residual where its rows are dense; other outputs that
+ * overlap an input or another output are refused. Errors: FME_OK, FME_EINVAL,
+ * FME_EALIGN, FME_ECUDA.
+ */
+int fme_block_norm(const void* x, long long ldx, const float* route_weights, int top_k, const void* shared_out,
+                   const void* post_gamma, const void* gate, long long ldg, const void* residual, long long ldr,
+                   float residual_scale, const void* gamma, int T, int H, float eps, int quant, int ue8m0, uint8_t* q,
+                   void* scales, void* normed, void* residual_out, void* stream);
+
+/*
+ * out = act(x W^T + bias) + residual in one launch: the router's product and a
+ * layer's dense projections (no counterpart in the pages). Sums, activation
+ * and residual addition are FP32, rounded once to the output's type.
+ *
+ * Arguments: x [M, K] BF16 with row stride ldx, w [N, K] BF16 with row stride
+ *   ldw, bias [N] FP32 or NULL, activation an fme_activation, residual [M, N]
+ *   of the output's type with row stride ldr, or NULL, out [M, N] of out_dtype
+ *   (FME_F32 or FME_BF16) with row stride ldo. 0 <= M <= 2^20 (0: nothing is
+ *   done), N and K in [1, 2^17]; ldx and ldw multiples of 8 and at least K, ldo
+ *   and ldr at least N, none above 2^34; x and w 16-byte aligned, the others to their element.
+ *   Rows whose ends are not multiples of 8 values are not read past K. out may
+ *   be residual with the same stride; out that overlaps an input otherwise is
+ *   refused. The workspace (fme_linear_bf16_workspace) must be zeroed before
+ *   its first use; it serves every product that needs no more. Errors:
+ *   FME_OK, FME_EINVAL, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA; device waits
+ *   that gave up set error bits 1 and 4 of the workspace.
+ */
+int fme_linear_bf16(const void* x, long long ldx, const void* w, long long ldw, const float* bias, int activation,
+                    const void* residual, long long ldr, int M, int N, int K, void* out, int out_dtype, long long ldo,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fme_linear_bf16 needs for these sizes on the current device (0 on bad sizes). */
+size_t fme_linear_bf16_workspace(int M, int N, int K);
 
 /* Zero a workspace (cudaMemsetAsync on stream). */
 int fme_workspace_clear(void* workspace, size_t workspace_bytes, void* stream);

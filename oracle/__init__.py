@@ -29,4 +29,4 @@ casts, brute force on tiny inputs, algebraic identities, invariants). No
 function is "parity unpinned".
 """
 
-from . import codecs, routing, quant, moe_fp8, moe_nvfp4, finalize, ep_local, prompt  # noqa: F401
+from . import codecs, routing, quant, moe_fp8, moe_nvfp4, finalize, ep_local, prompt, linear  # noqa: F401

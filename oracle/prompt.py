@@ -59,3 +59,43 @@ def grouped_product(a, sa, w, sw, offsets, in_rows=None):
             y[lo:hi] += A[r, b] @ W[:, b].T * s
             size[lo:hi] += np.abs(A[r, b]) @ np.abs(W[:, b]).T * np.abs(s)
     return y, size
+
+
+def block_norm(x, gamma, residual=None, route_weights=None, shared_out=None, post_gamma=None, gate=None,
+               residual_scale=1.0, eps=1e-5):
+    """(h, y, dh, dy) float64: what stands between a block and the next. o = x, or the weighted sum of each token's
+    routes (+ shared_out); p = o / sqrt(mean o^2 + eps) * post_gamma; h = residual_scale * residual + gate * p; y = h /
+    sqrt(mean h^2 + eps) * gamma; nothing rounded. dh and dy bound what FP32 arithmetic may be off (u = 2^-24):
+    a sum of n terms by n u of their magnitudes, a row's mean square, of sums of at most 64 terms, by 80 u and what its
+    values are off, each product and addition by u."""
+    u = 2.0 ** -24
+    f = lambda v: None if v is None else np.asarray(v, dtype=np.float64)  # noqa: E731
+    x, gamma, residual, w, shared_out, post_gamma, gate = map(f, (x, gamma, residual, route_weights, shared_out,
+                                                                   post_gamma, gate))
+
+    def norm(v, dv, g):
+        r = 1 / np.sqrt((v * v).mean(axis=1, keepdims=True) + eps)
+        length = np.sqrt((v * v).sum(axis=1, keepdims=True))
+        off = np.sqrt((dv * dv).sum(axis=1, keepdims=True)) / np.where(length > 0, length, 1.0)
+        return v * r * g, (dv * r + np.abs(v) * r * (48 * u + off)) * np.abs(g)
+
+    o, do = x, np.zeros_like(x)
+    if w is not None:
+        T, k = w.shape
+        terms = x.reshape(T, k, -1) * w[:, :, None]
+        o, size = terms.sum(axis=1), np.abs(terms).sum(axis=1)
+        if shared_out is not None:
+            o, size = o + shared_out, size + np.abs(shared_out)
+        do = (k + 3) * u * size
+    if post_gamma is not None:
+        o, do = norm(o, do, post_gamma)
+    if gate is not None:
+        o, do = o * gate, do * np.abs(gate) + u * np.abs(o * gate)
+    h, dh = o, do
+    if residual is not None:
+        h = h + residual_scale * residual
+        dh = dh + u * (np.abs(residual_scale * residual) + np.abs(h))
+    if gamma is None:
+        return h, None, dh, None
+    y, dy = norm(h, dh, gamma)
+    return h, y, dh, dy

@@ -76,3 +76,51 @@ def selection_gap(keys, ids) -> np.ndarray:
         for a, b in zip(ordered, ordered[1:]):
             gaps[t] = min(gaps[t], a - b)
     return gaps
+
+
+def route_groups(logits, bias, top_k, score="sigmoid", groups=1, top_groups=1, group_top=1, renormalise=True, scale=1.0):
+    """Routing with sigmoid or softmax scores and the experts of each token's top_groups best of `groups` equal runs (a run
+    counts as the sum of its best group_top keys), in float64.
+
+    Keys are score + bias; without a bias the logits, whose order is the scores', and a group's sum is of logits with
+    group_top 1 and of scores with 2. Ties go to the lower expert or group. Returns ids [M, top_k], weights [M, top_k]
+    float64 and gaps [M]: the smallest gap, relative to the larger value, that decides a token's groups or picks and is
+    not an exact tie."""
+    l = np.asarray(logits, dtype=np.float64)
+    M, E = l.shape
+    size = E // groups
+    with np.errstate(over="ignore", invalid="ignore"):
+        if score == "softmax":
+            m = l.max(axis=1, keepdims=True)
+            e = np.exp(l - np.where(np.isfinite(m), m, 0.0))
+            total = e.sum(axis=1, keepdims=True)
+            p = np.where(total > 0, e / np.where(total > 0, total, 1.0), 0.0)
+        else:
+            p = 1.0 / (1.0 + np.exp(-l))
+    ids = np.empty((M, top_k), dtype=np.int32)
+    weights = np.zeros((M, top_k))
+    gaps = np.full(M, np.inf)
+
+    def note(t, a, b):
+        if a != b and np.isfinite(a) and np.isfinite(b):
+            gaps[t] = min(gaps[t], (a - b) / max(abs(a), abs(b)))
+
+    for t in range(M):
+        key = l[t] if bias is None else p[t] + np.asarray(bias, dtype=np.float64)
+        open_ = range(groups)
+        if top_groups < groups:
+            by = p[t] if bias is None and group_top == 2 else key
+            sums = [sum(sorted(by[g * size:(g + 1) * size], reverse=True)[:group_top]) for g in range(groups)]
+            order = sorted(range(groups), key=lambda g: (-sums[g], g))
+            note(t, sums[order[top_groups - 1]], sums[order[top_groups]])
+            open_ = order[:top_groups]
+        experts = [e for g in open_ for e in range(g * size, (g + 1) * size)]
+        order = sorted(experts, key=lambda e: (-key[e], e))
+        for a, b in zip(order[:top_k], order[1:top_k + 1]):
+            note(t, key[a], key[b])
+        ids[t] = order[:top_k]
+        w = p[t][ids[t]]
+        if renormalise:
+            w = w / w.sum() if w.sum() > 0 else 0.0 * w
+        weights[t] = w * scale
+    return ids, weights, gaps
