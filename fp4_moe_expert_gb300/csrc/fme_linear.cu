@@ -1,17 +1,32 @@
 // out = act(x W^T + bias) + residual, BF16 x [M, K] and W [N, K], FP32 sums, one rounding to the output's type.
 //
-// Two kernels.
+// Three kernels.
 //
-// Up to kLnRowsMax tokens, linear_rows_kernel: a warp (or 2, 4, 8 that share its K range) holds kLnRows weight rows' sums
-// for every token in registers, 16 bytes of a row a lane and load. Bound by the weights' stream, and by latency where they
-// are few.
+// linear_one_kernel, one token: a warp (or 2, 4, 8 that share its K range) multiplies kLnRows weight rows, 16 bytes of each
+// a lane and load. Bound by latency where the weights are few (256 x 7168: 2.7 us) and by their stream where they are many
+// (4096 x 7168: 13 us, 4.4 TB/s).
 //
-// Above, linear_tc_kernel: one persistent CTA per SM walks units, tiles of 128 tokens x tile_n weight rows (a multiple of
-// 16 up to 256) times a share of K. Ten warps: one loads by TMA (64 values of the tile's rows a stage, 128-byte swizzle),
-// one issues tcgen05.mma kind::f16, eight read the accumulators (two buffers in tensor memory, so that a tile's epilogue
-// runs beside the next tile's products). Where the tiles are fewer than SMs, K is cut, too: a unit then stores its FP32
-// sums to the workspace and the last of a tile's units to arrive adds them in K order, whichever it is, so the result
-// does not hang on the order of arrival, and no unit waits for another.
+// linear_few_kernel, up to 16 tokens (ln_few): warps hold 16 tokens x 8 weight rows in mma.sync fragments, loaded straight
+// from global memory. A tcgen05 tile needs its operands in shared memory, tensor memory allocated and a pipeline filled,
+// which is 5 us before the first result; here 8 tokens of 256 x 7168 take 4.6 us instead of 11.1.
+//
+// linear_tc_kernel, the rest: one persistent CTA per SM walks units, tiles of up to 128 tokens x tile_n weight rows (a
+// multiple of 16 up to 256) times a share of K. Twelve warps: two load by TMA (tokens and weights, 128-byte swizzle), one
+// issues tcgen05.mma kind::f16, eight read the accumulators (two buffers in tensor memory, so that a tile's epilogue runs
+// beside the next tile's products). Where the tiles are fewer than SMs, K is cut, too: a unit then stores its FP32 sums to
+// the workspace and the last of a tile's units to arrive adds them in K order, whichever it is, so the result does not hang
+// on the order of arrival, and no unit waits for another.
+// * A stage holds as many K blocks of 64 values as fit 64 KB: a TMA instruction costs its warp about 100 ns whatever it
+//   brings (16 tokens x 7168 x 2048: 12.3 us with one block a stage and one loading warp, 7.8 with eight and two).
+// * FP32 outputs: the tensor core's accumulation truncates, so a chain of 448 instructions (K = 7168) is 8e-6 of the result
+//   off. Accumulations of kLnChunk blocks are added in registers with rounding instead: 5e-7, at 57.5 us instead of 53.8
+//   (16384 x 256 x 7168). BF16 outputs, whose rounding is 250 times that, take the chain.
+// What bounds it: large products the operands' way into shared memory, 48 KB a block in 694 clocks against 512 of MMA
+// (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a burst; the tiles' order counts, 771 us with the row tiles of one
+// weight tile one after another). Measured and left out: 256 x 256 tiles, two accumulators that share the weights, three
+// stages of 64 KB (626 us against 577); prefetches into L2 ahead of the ring (router of 16384 tokens 57.8 against 57.4 us,
+// 64 x 4096 x 7168 18.1 against 17.4); CTAs that start at different places of K (no difference); two CTAs an SM with
+// half the ring (64 x 7168 x 2048 11.2 us against 9.1).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -28,7 +43,7 @@ struct LnEpilogue {
   long long ldr, ldo;
   void* out;
   int act, out_f32;
-  int wide;  // out (and residual) rows start at multiples of 32 bytes: whole sectors a store
+  int wide;  // bytes that out (and residual) rows start at multiples of, where those are 32 or 16
   int M, N;
 };
 
@@ -63,16 +78,27 @@ __device__ __forceinline__ void ln_store(const LnEpilogue& e, float z, int row, 
   }
 }
 
-__device__ __forceinline__ void ln_st32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+__device__ __forceinline__ void ln_st32(void* p, const uint32_t (&w)[8], bool sector) {
+  if (sector) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
-__device__ __forceinline__ void ln_ld32(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
+__device__ __forceinline__ void ln_ld32(const void* p, uint32_t (&w)[8], bool sector) {
+  if (sector) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 lo = static_cast<const uint4*>(p)[0], hi = static_cast<const uint4*>(p)[1];
+    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+    w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+  }
 }
 __device__ __forceinline__ uint32_t ln_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -80,39 +106,59 @@ __device__ __forceinline__ uint32_t ln_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Sixteen sums of one row, columns n .. n + 15 (those below N).
-__device__ __forceinline__ void ln_store16(const LnEpilogue& e, float (&z)[16], int row, int n) {
-  if (!e.wide || n + 16 > e.N) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n + i < e.N) ln_store(e, z[i], row, n + i);
-    return;
+// ln_act for outputs of 8 bits' precision: exp and reciprocal by the hardware's approximations (a few 2^-22).
+__device__ __forceinline__ float ln_recip_approx(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+__device__ __forceinline__ float ln_act_bf16(float z, int act) {
+  switch (act) {
+    case FME_ACT_SILU:
+      return __fmul_rn(z, ln_recip_approx(__fadd_rn(1.0f, __expf(-z))));
+    case FME_ACT_SIGMOID:
+      return ln_recip_approx(__fadd_rn(1.0f, __expf(-z)));
+    default:
+      return ln_act(z, act);
   }
+}
+
+// Sixteen sums of one row, columns n .. n + 15 (bias and activation).
+__device__ __forceinline__ void ln_finish16(const LnEpilogue& e, float (&z)[16], int n) {
   if (e.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], __ldg(e.bias + n + i));
+    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], n + i < e.N ? __ldg(e.bias + n + i) : 0.0f);
   }
-  if (e.act != FME_ACT_NONE) {
+  if (e.act == FME_ACT_NONE) return;
+  if (e.out_f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], e.act);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = ln_act_bf16(z[i], e.act);
   }
+}
+
+// Adds the residual to sixteen values of one row and stores them, 32 or 16 bytes at a time.
+__device__ __forceinline__ void ln_store16(const LnEpilogue& e, float (&z)[16], int row, int n) {
   const size_t r = static_cast<size_t>(row) * e.ldr + n, o = static_cast<size_t>(row) * e.ldo + n;
+  const bool sector = e.wide == 32;
   uint32_t w[8];
   if (e.out_f32) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (e.residual != nullptr) {
-        ln_ld32(static_cast<const float*>(e.residual) + r + 8 * h, w);
+        ln_ld32(static_cast<const float*>(e.residual) + r + 8 * h, w, sector);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[8 * h + i] = __fadd_rn(z[8 * h + i], __uint_as_float(w[i]));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z[8 * h + i]);
-      ln_st32(static_cast<float*>(e.out) + o + 8 * h, w);
+      ln_st32(static_cast<float*>(e.out) + o + 8 * h, w, sector);
     }
   } else {
     if (e.residual != nullptr) {
-      ln_ld32(static_cast<const __nv_bfloat16*>(e.residual) + r, w);
+      ln_ld32(static_cast<const __nv_bfloat16*>(e.residual) + r, w, sector);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         z[2 * i] = __fadd_rn(z[2 * i], __uint_as_float(w[i] << 16));
@@ -121,12 +167,45 @@ __device__ __forceinline__ void ln_store16(const LnEpilogue& e, float (&z)[16], 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = ln_bf16x2(z[2 * i], z[2 * i + 1]);
-    ln_st32(static_cast<__nv_bfloat16*>(e.out) + o, w);
+    ln_st32(static_cast<__nv_bfloat16*>(e.out) + o, w, sector);
   }
 }
 
-// ---------------------------------------------------------------- a few tokens
-constexpr int kLnRowsMax = 8;   // most tokens
+// The same for a warp's 32 rows (from `row`, the first `rows` of them) whose starts do not suit whole sectors, or of which
+// only the first `cols` columns exist: turned through shared memory, so that neighbouring lanes store neighbouring
+// values (1533 x 895 outputs: see linear_tc_kernel).
+__device__ __forceinline__ void ln_store_turned(const LnEpilogue& e, const float (&z)[16], float* turn, int row, int rows,
+                                                int n, int cols, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) turn[lane * 17 + i] = z[i];
+  __syncwarp();
+  const int col = lane & 15, r0 = lane >> 4;
+  if (col >= cols) return;
+  // All loads before the first store: the compiler cannot know that they do not meet.
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = turn[(2 * i + r0) * 17 + col];
+  const size_t from = static_cast<size_t>(row + r0) * e.ldr + n + col, to = static_cast<size_t>(row + r0) * e.ldo + n + col;
+  if (e.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + r0 < rows)
+        v[i] = __fadd_rn(v[i], e.out_f32 ? static_cast<const float*>(e.residual)[from + 2 * i * e.ldr]
+                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[from + 2 * i * e.ldr]));
+  }
+  if (e.out_f32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + r0 < rows) static_cast<float*>(e.out)[to + 2 * i * e.ldo] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + r0 < rows) static_cast<__nv_bfloat16*>(e.out)[to + 2 * i * e.ldo] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// ---------------------------------------------------------------- one token
 constexpr int kLnRows = 2;      // weight rows a warp
 constexpr int kLnRowWarps = 8;  // warps a CTA
 
@@ -158,87 +237,153 @@ __device__ __forceinline__ uint4 ln_chunk(const __nv_bfloat16* row, int c, int K
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int MT>
-__global__ void __launch_bounds__(32 * kLnRowWarps) linear_rows_kernel(const LnRowsArgs a) {
-  __shared__ float part[kLnRowWarps][kLnRows * MT];
+__global__ void __launch_bounds__(32 * kLnRowWarps) linear_one_kernel(const LnRowsArgs a) {
+  __shared__ float part[kLnRowWarps][kLnRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = kLnRowWarps / a.share;  // of warps, kLnRows weight rows each
   const int n0 = (blockIdx.x * groups + warp / a.share) * kLnRows;
   griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
-  float acc[kLnRows][MT];
+  float acc[kLnRows];
 #pragma unroll
-  for (int r = 0; r < kLnRows; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[r][m] = 0.0f;
+  for (int r = 0; r < kLnRows; ++r) acc[r] = 0.0f;
   if (n0 < a.e.N) {
     const int chunks = (a.K + 7) / 8;
-    // (Past the last weight or token row: the last again, dropped below.)
-    const __nv_bfloat16* w[kLnRows];
+    const __nv_bfloat16* w[kLnRows];  // (past the last row: the last again, dropped below)
 #pragma unroll
     for (int r = 0; r < kLnRows; ++r) w[r] = a.w + min(n0 + r, a.e.N - 1) * a.ldw;
 #pragma unroll 4
     for (int c = (warp % a.share) * 32 + lane; c < chunks; c += 32 * a.share) {
-      uint4 wp[kLnRows];
+      float wv[kLnRows][8], xv[8];
 #pragma unroll
-      for (int r = 0; r < kLnRows; ++r) wp[r] = ln_chunk(w[r], c, a.K);
-      float wv[kLnRows][8];
+      for (int r = 0; r < kLnRows; ++r) ln_unpack(ln_chunk(w[r], c, a.K), wv[r]);
+      ln_unpack(ln_chunk(a.x, c, a.K), xv);
 #pragma unroll
-      for (int r = 0; r < kLnRows; ++r) ln_unpack(wp[r], wv[r]);
+      for (int r = 0; r < kLnRows; ++r)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float xv[8];
-        ln_unpack(ln_chunk(a.x + min(m, a.e.M - 1) * a.ldx, c, a.K), xv);
-#pragma unroll
-        for (int r = 0; r < kLnRows; ++r)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[r][m] = __fmaf_rn(xv[k], wv[r][k], acc[r][m]);
-      }
+        for (int k = 0; k < 8; ++k) acc[r] = __fmaf_rn(xv[k], wv[r][k], acc[r]);
     }
 #pragma unroll
     for (int r = 0; r < kLnRows; ++r)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-          acc[r][m] = __fadd_rn(acc[r][m], __shfl_xor_sync(0xFFFFFFFFu, acc[r][m], d));
+      for (int d = 16; d >= 1; d >>= 1) acc[r] = __fadd_rn(acc[r], __shfl_xor_sync(0xFFFFFFFFu, acc[r], d));
   }
   if (lane == 0)
 #pragma unroll
-    for (int r = 0; r < kLnRows; ++r)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) part[warp][r * MT + m] = acc[r][m];
+    for (int r = 0; r < kLnRows; ++r) part[warp][r] = acc[r];
   __syncthreads();
-  for (int i = threadIdx.x; i < groups * kLnRows * MT; i += 32 * kLnRowWarps) {
-    const int r = i % kLnRows, g = i / kLnRows % groups, m = i / (kLnRows * groups);
+  if (threadIdx.x < groups * kLnRows) {
+    const int r = threadIdx.x % kLnRows, g = threadIdx.x / kLnRows;
     const int n = (blockIdx.x * groups + g) * kLnRows + r;
-    if (n >= a.e.N || m >= a.e.M) continue;
+    if (n < a.e.N) {
+      float z = 0.0f;
+      for (int s = 0; s < a.share; ++s) z = __fadd_rn(z, part[g * a.share + s][r]);
+      ln_store(a.e, z, 0, n);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- a few tokens
+constexpr int kLnFewMax = 16;    // most tokens
+constexpr int kLnFewWarps = 16;  // warps a CTA
+constexpr int kLnFewSteps = 4;   // steps of 32 values that a warp loads at once
+
+// D += A B^T, 16 tokens x 8 weight rows x 16 values of K, in registers.
+__device__ __forceinline__ void ln_mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// share: warps that share a weight row's K range (1 to 16, a power of two). BOTH: more than 8 tokens.
+template <bool BOTH>
+__global__ void __launch_bounds__(32 * kLnFewWarps) linear_few_kernel(const LnRowsArgs a) {
+  __shared__ float part[kLnFewWarps][16][8];  // [token][weight row]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int groups = kLnFewWarps / a.share;  // of 8 weight rows
+  const int n0 = (blockIdx.x * groups + warp / a.share) * 8;
+  griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
+  griddep_wait();
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n0 < a.e.N) {
+    // A lane's fragments are 8 neighbouring values of token g (and g + 8) and weight row g: which of the instruction's K
+    // slots they take is the same for both, so their order does not matter. (Past the last row: the last again, dropped
+    // below.)
+    const __nv_bfloat16* w = a.w + min(n0 + g, a.e.N - 1) * a.ldw;
+    const __nv_bfloat16* x0 = a.x + min(g, a.e.M - 1) * a.ldx;
+    const __nv_bfloat16* x1 = a.x + min(g + 8, a.e.M - 1) * a.ldx;
+    const int steps = (a.K + 31) / 32;
+    for (int s = warp % a.share; s < steps; s += kLnFewSteps * a.share) {
+      uint4 wp[kLnFewSteps], xp[kLnFewSteps], yp[kLnFewSteps];
+#pragma unroll
+      for (int i = 0; i < kLnFewSteps; ++i) {
+        wp[i] = xp[i] = yp[i] = make_uint4(0, 0, 0, 0);
+        const int c = 4 * (s + i * a.share) + q;
+        if (s + i * a.share < steps) {
+          wp[i] = ln_chunk(w, c, a.K);
+          xp[i] = ln_chunk(x0, c, a.K);
+          if (BOTH) yp[i] = ln_chunk(x1, c, a.K);
+        }
+      }
+      // Chains of eight instructions in the tensor core, which truncates; their sums are added with rounding.
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kLnFewSteps; ++i) {
+        ln_mma_16x8(d, xp[i].x, yp[i].x, xp[i].y, yp[i].y, wp[i].x, wp[i].y);
+        ln_mma_16x8(d, xp[i].z, yp[i].z, xp[i].w, yp[i].w, wp[i].z, wp[i].w);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[k] = __fadd_rn(sum[k], d[k]);
+    }
+  }
+  part[warp][g][2 * q] = sum[0];
+  part[warp][g][2 * q + 1] = sum[1];
+  part[warp][g + 8][2 * q] = sum[2];
+  part[warp][g + 8][2 * q + 1] = sum[3];
+  __syncthreads();
+  for (int i = threadIdx.x; i < groups * 8 * a.e.M; i += 32 * kLnFewWarps) {
+    const int r = i % 8, m = i / 8 % a.e.M, grp = i / (8 * a.e.M);
+    const int n = (blockIdx.x * groups + grp) * 8 + r;
+    if (n >= a.e.N) continue;
     float z = 0.0f;
-    for (int s = 0; s < a.share; ++s) z = __fadd_rn(z, part[g * a.share + s][r * MT + m]);
+    for (int s = 0; s < a.share; ++s) z = __fadd_rn(z, part[grp * a.share + s][m][r]);
     ln_store(a.e, z, m, n);
   }
 }
 
 // ---------------------------------------------------------------- tiles
-constexpr int kLnThreads = 320;
+constexpr int kLnThreads = 384;
 constexpr int kLnEpiWarps = 8;
+// Registers a thread: 384 x 168 at launch, then 8 epilogue warps x 216 and 4 others x 72 (the same sum): a thread of the
+// epilogue holds 128 sums.
+constexpr int kLnLaunchRegs = 168, kLnEpiRegs = 216, kLnOtherRegs = 72;
+static_assert(2 * kLnEpiRegs + kLnOtherRegs == 3 * kLnLaunchRegs, "register split");
 constexpr int kLnMaxUnits = 160;           // units of a call that cuts K (one a CTA)
 constexpr int kLnKBlock = 64;              // values a stage: 128 bytes a row
-constexpr int kLnABytes = 128 * 128;       // a stage's token rows
 constexpr int kLnMaxStages = 12;
-constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows, 10 of 128 + 16
+constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows
+constexpr int kLnStageBytes = 65536;
+constexpr int kLnChunk = 8;
+constexpr int kLnGroup = 8;                // weight tiles that are walked together
 constexpr int kLnHeader = 4096;            // workspace: error word, then from byte 256 the tiles' arrival counters
 
 struct LnTcArgs {
-  CUtensorMap mapx;  // x [M, K], box box_m rows x 64 values
-  CUtensorMap mapw;  // w [N, K], box tile_n rows x 64 values
-  int box_m, tile_n, tiles_m, tiles_n;
+  CUtensorMap mapx, mapx1;  // x [M, K], box box_m rows x 64 values, `slices` (1) K blocks of them
+  CUtensorMap mapw, mapw1;  // w [N, K], box tile_n rows x 64 values, likewise
+  int tile_m, box_m, tile_n, tiles_m, tiles_n;
   int blocks;  // K blocks of a row
+  int slices;  // K blocks a stage
+  int groups;  // stages of a row
+  int single;  // first stage that is loaded block by block
+  int chunk;   // stages that one accumulation in tensor memory takes
   int split;   // units a tile
   int units, stages;
   uint32_t tmem_cols;  // allocated: both buffers
   float* partial;      // [units][tile_n][rows]
-  int rows;            // rows of a partial tile: min(M, 128)
+  int rows;            // rows of a partial tile
   uint32_t* err;
   uint32_t* arrived;  // [tiles], zero between calls
   unsigned long long timeout_ns;
@@ -254,8 +399,11 @@ struct LnShared {
   uint32_t tmem;
   int abort;
   int last;
+  float turn[kLnEpiWarps][32 * 17];
 };
 constexpr size_t kLnSmemBytes = kLnRingBytes + 1024 + sizeof(LnShared);
+static_assert(kLnSmemBytes <= 232448, "shared memory per CTA");
+static_assert(sizeof(LnShared) >= 128 * 128, "an MMA of the last stage reads 128 rows");
 
 // Instruction descriptor of tcgen05.mma kind::f16 with BF16 A and B, both K-major, FP32 accumulation, shape 128 x N.
 __device__ __forceinline__ uint32_t ln_idesc(int N) {
@@ -271,29 +419,37 @@ __device__ __forceinline__ void ln_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
 }
 
 struct LnUnit {
-  int m, n, tile, kb0, kb1;
+  int m, n, tile, g0, g1;  // tile, and the unit's stages of K
 };
 __device__ __forceinline__ LnUnit ln_unit(const LnTcArgs& a, int u) {
   LnUnit t;
   t.tile = u / a.split;
   const int s = u - t.tile * a.split;
-  t.n = t.tile / a.tiles_m;
-  t.m = t.tile - t.n * a.tiles_m;
-  t.kb0 = static_cast<int>(static_cast<long long>(s) * a.blocks / a.split);
-  t.kb1 = static_cast<int>(static_cast<long long>(s + 1) * a.blocks / a.split);
+  // Weight tiles in groups of kLnGroup, within a group the tiles of one row tile are neighbours: CTAs running at the same
+  // time share both operands through L2.
+  const int each = kLnGroup * a.tiles_m, g = t.tile / each, in = t.tile - g * each;
+  const int width = min(kLnGroup, a.tiles_n - g * kLnGroup);
+  t.m = in / width;
+  t.n = g * kLnGroup + in - t.m * width;
+  t.g0 = s * a.groups / a.split;
+  t.g1 = (s + 1) * a.groups / a.split;
   return t;
 }
 
+template <bool CHUNKED>
 __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_constant__ LnTcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   LnShared& S = *reinterpret_cast<LnShared*>(ring + kLnRingBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t stage_bytes = kLnABytes + a.tile_n * 128;
+  // A stage: its blocks' token rows, then its blocks' weight rows. The MMA reads 128 token rows whatever the box has: what it
+  // finds past them (other rows, at the ring's end this CTA's variables) goes to rows that are not stored.
+  const uint32_t a_block = a.box_m * 128, b_block = a.tile_n * 128;
+  const uint32_t a_bytes = a.slices * a_block, stage_bytes = a_bytes + a.slices * b_block;
 
   if (tid == 0) {
     for (int s = 0; s < kLnMaxStages; ++s) {
-      mbar_init(&S.full[s], 1);
+      mbar_init(&S.full[s], 2);
       mbar_init(&S.done[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -304,11 +460,11 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     S.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 9) {
     tmem_alloc(&S.tmem, a.tmem_cols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     prefetch_tmap(&a.mapx);
     prefetch_tmap(&a.mapw);
   }
@@ -321,34 +477,45 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
   const volatile int* abort = &S.abort;
   const int first = blockIdx.x, step = gridDim.x;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
+  if (CHUNKED && warp >= kLnEpiWarps) reg_dec<kLnOtherRegs>();
+
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------------------ loads: one warp the tokens, the other the weights
+    const bool tokens = warp == 8;
+    const uint32_t block_bytes = tokens ? a_block : b_block;
+    const CUtensorMap* map = tokens ? &a.mapx : &a.mapw;
+    const CUtensorMap* map1 = tokens ? &a.mapx1 : &a.mapw1;
     uint32_t it = 0, s = 0, phase = 0;
     bool ok = true;
-    const uint32_t bytes = (a.box_m + a.tile_n) * 128;
     for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
-      for (int j = t.kb0; j < t.kb1; ++j, ++it) {
+      const int y = tokens ? a.tile_m * t.m : a.tile_n * t.n;
+      for (int g = t.g0; g < t.g1; ++g, ++it) {
         ok = mbar_wait_spin(&S.done[s], phase ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        uint8_t* st = ring + s * stage_bytes;
+        uint8_t* st = ring + s * stage_bytes + (tokens ? 0 : a_bytes);
+        const int j = g * a.slices;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&S.full[s], bytes);
-          tma_load_2d(st, &a.mapx, kLnKBlock * j, 128 * t.m, &S.full[s]);
-          tma_load_2d(st + kLnABytes, &a.mapw, kLnKBlock * j, a.tile_n * t.n, &S.full[s]);
+          if (g >= a.single) {
+            const int n = min(a.slices, a.blocks - j);
+            mbar_arrive_expect_tx(&S.full[s], n * block_bytes);
+            for (int k = 0; k < n; ++k) tma_load_2d(st + k * block_bytes, map1, kLnKBlock * (j + k), y, &S.full[s]);
+          } else {
+            mbar_arrive_expect_tx(&S.full[s], a.slices * block_bytes);
+            tma_load_3d(st, map, 0, y, j, &S.full[s]);
+          }
         }
         __syncwarp();
         if (++s == static_cast<uint32_t>(a.stages)) s = 0, phase ^= 1;
       }
     }
     // The last stages' arrivals have to land before the CTA leaves its shared memory: the MMAs' of a good end, the
-    // copies' of a bad one (given 10 ms each, a thousand times a copy's latency).
+    // copies' of a bad one (given 10 ms each, a thousand times a copy's latency: the other loads may be missing).
     if (lane == 0) {
       const uint32_t n = a.stages;
       for (uint32_t k = it > n ? it - n : 0; k < it; ++k) {
-        if (ok)
-          ok = mbar_wait_spin(&S.done[k % n], (k / n) & 1, a.timeout_ns, abort);
+        if (ok) ok = mbar_wait_spin(&S.done[k % n], (k / n) & 1, a.timeout_ns, abort);
         if (!ok) mbar_wait_spin(&S.full[k % n], (k / n) & 1, 10000000ull, nullptr);
       }
       if (!ok) {
@@ -357,32 +524,38 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ MMA
-    uint32_t s = 0, phase = 0, n = 0;
+    uint32_t s = 0, phase = 0, n = 0;  // n: accumulations begun
     bool ok = true;
     const uint32_t idesc = ln_idesc(a.tile_n);
     const uint64_t desc0 = sw128_desc(smem_u32(ring));
-    for (int u = first; u < a.units && ok; u += step, ++n) {
+    for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
-      const uint32_t b = n & 1, d = tmem + b * (a.tmem_cols / 2);
-      ok = mbar_wait_spin(&S.tempty[b], ((n >> 1) & 1) ^ 1, a.timeout_ns, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      for (int j = t.kb0; j < t.kb1 && ok; ++j) {
-        ok = mbar_wait_spin(&S.full[s], phase, a.timeout_ns, abort);
+      for (int c0 = t.g0; c0 < t.g1 && ok; c0 += a.chunk, ++n) {
+        const int c1 = min(t.g1, c0 + a.chunk);
+        const uint32_t b = n & 1, d = tmem + b * (a.tmem_cols / 2);
+        ok = mbar_wait_spin(&S.tempty[b], ((n >> 1) & 1) ^ 1, a.timeout_ns, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          // The start address is the descriptor's low field, in units of 16 bytes.
-          const uint64_t ad = desc0 + ((s * stage_bytes) >> 4), bd = ad + (kLnABytes >> 4);
+        for (int g = c0; g < c1 && ok; ++g) {
+          ok = mbar_wait_spin(&S.full[s], phase, a.timeout_ns, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const int blocks = min(a.slices, a.blocks - g * a.slices);
+          if (elect_one()) {
+            // The start address is the descriptor's low field, in units of 16 bytes.
+            uint64_t ad = desc0 + ((s * stage_bytes) >> 4), bd = ad + (a_bytes >> 4);
+#pragma unroll 1
+            for (int j = 0; j < blocks; ++j, ad += a_block >> 4, bd += b_block >> 4)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ln_mma(d, ad + 2 * i, bd + 2 * i, idesc, j > t.kb0 || i != 0);
-          tc_commit(&S.done[s]);
-          if (j == t.kb1 - 1) tc_commit(&S.tfull[b]);
+              for (int i = 0; i < 4; ++i) ln_mma(d, ad + 2 * i, bd + 2 * i, idesc, g > c0 || j + i != 0);
+            tc_commit(&S.done[s]);
+            if (g == c1 - 1) tc_commit(&S.tfull[b]);
+          }
+          __syncwarp();
+          if (++s == static_cast<uint32_t>(a.stages)) s = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++s == static_cast<uint32_t>(a.stages)) s = 0, phase ^= 1;
       }
     }
     if (!ok && elect_one()) {
@@ -392,71 +565,119 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       if (!mbar_wait_spin(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
     }
     __syncwarp();
-  } else {
+  } else if (warp < kLnEpiWarps) {
     // ------------------------------------------------------------ epilogue
+    if (CHUNKED) reg_inc<kLnEpiRegs>();
     // A warp reads the 32 tensor-memory lanes (rows) its number allows; the two warps of a quarter share the columns.
-    const int quad = warp & 3, half = (warp - 2) >> 2, etid = tid - 64;
+    const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;
+    float* turn = S.turn[warp];
     uint32_t n = 0;
     bool ok = true;
-    for (int u = first; u < a.units && ok; u += step, ++n) {
+    for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
-      const uint32_t b = n & 1;
-      ok = mbar_wait_spin(&S.tfull[b], (n >> 1) & 1, a.timeout_ns, abort);
-      // Uniform over the eight warps, so that none is left waiting at a barrier below.
-      ok = !named_bar_or(1, 32 * kLnEpiWarps, !ok);
+      const int m0 = a.tile_m * t.m, n0 = a.tile_n * t.n;
+      const int rows = min(a.tile_m, a.e.M - m0) - 32 * quad;  // of this warp's 32
+      uint32_t base = 0;  // this thread's row of the accumulator, from the columns of its half
+      auto wait = [&]() {
+        ok = mbar_wait_spin(&S.tfull[n & 1], (n >> 1) & 1, a.timeout_ns, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        base = tmem + (n & 1) * (a.tmem_cols / 2) + (static_cast<uint32_t>(32 * quad) << 16) + 16 * half;
+        return ok;
+      };
+      auto release = [&]() {  // the MMA may write the buffer again
+        __syncwarp();
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(&S.tempty[n & 1]);
+        ++n;
+      };
+      if (CHUNKED) {
+        // The accumulations' sums meet in registers, 16 columns 32 i + 16 half each; the tile's go back over the last one's.
+        float z[8][16];
+        for (int c0 = t.g0; c0 < t.g1; c0 += a.chunk) {
+          if (!wait()) break;
+          if (rows > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (32 * i + 16 * half < a.tile_n) {
+                float d[16];
+                tmem_ld_issue(base + 32 * i, d);
+                tmem_ld_join(d);
+                if (c0 == t.g0) {
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) z[i][k] = d[k];
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) z[i][k] = __fadd_rn(z[i][k], d[k]);
+                }
+                if (c0 + a.chunk >= t.g1) tmem_st16(base + 32 * i, reinterpret_cast<const uint32_t(&)[16]>(z[i]));
+              }
+          }
+          if (c0 + a.chunk < t.g1) release();
+        }
+        tc_wait_st();
+      } else {
+        wait();
+      }
+      // Uniform over the eight warps where a barrier follows, so that none is left waiting there.
+      if (a.split > 1) ok = !named_bar_or(1, 32 * kLnEpiWarps, !ok);
       if (!ok) break;
-      tc_fence_after();
-      const uint32_t base = tmem + b * (a.tmem_cols / 2) + (static_cast<uint32_t>(32 * quad) << 16);
-      const int m = 128 * t.m + row, n0 = a.tile_n * t.n;
-      const bool live = 128 * t.m + 32 * quad < a.e.M;  // this warp has rows
-      float* part = a.partial + static_cast<size_t>(u) * a.tile_n * a.rows + row;
-      if (live) {
-        for (int c = 16 * half; c < a.tile_n; c += 32) {
-          float z[16];
-          tmem_ld_issue(base + c, z);
-          tmem_ld_join(z);
-          if (a.split > 1) {
+      bool mine = true;  // this unit finishes the tile
+      const size_t each = static_cast<size_t>(a.tile_n) * a.rows;
+      float* tile = a.partial + static_cast<size_t>(t.tile) * a.split * each + 16 * half * a.rows + row;
+      if (a.split > 1) {
+        float* part = tile + (u - t.tile * a.split) * each;
+        if (rows > 0)
+          for (int c = 0; c + 16 * half < a.tile_n; c += 32) {
+            float z[16];
+            tmem_ld_issue(base + c, z);
+            tmem_ld_join(z);
             if (row < a.rows) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) __stcg(part + static_cast<size_t>(c + i) * a.rows, z[i]);
+              for (int k = 0; k < 16; ++k) __stcg(part + (c + k) * a.rows, z[k]);
             }
-          } else if (m < a.e.M && n0 + c < a.e.N) {
-            ln_store16(a.e, z, m, n0 + c);
+          }
+        __threadfence();
+        named_bar_sync(1, 32 * kLnEpiWarps);
+        if (tid == 0) {
+          __threadfence();
+          S.last = atomicAdd(a.arrived + t.tile, 1u) == static_cast<uint32_t>(a.split) - 1u;
+          if (S.last) a.arrived[t.tile] = 0u;
+          __threadfence();
+        }
+        named_bar_sync(1, 32 * kLnEpiWarps);
+        mine = S.last;
+        __threadfence();
+      }
+      if (mine && rows > 0) {
+        for (int c = 0; c + 16 * half < a.tile_n; c += 32) {
+          const int col = n0 + c + 16 * half;
+          float z[16];
+          if (a.split == 1) {
+            tmem_ld_issue(base + c, z);
+            tmem_ld_join(z);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[k] = 0.0f;
+            if (row < a.rows) {
+              const float* from = tile + c * a.rows;
+#pragma unroll 4
+              for (int s = 0; s < a.split; ++s)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) z[k] = __fadd_rn(z[k], __ldcg(from + s * each + k * a.rows));
+            }
+          }
+          if (col >= a.e.N) break;
+          ln_finish16(a.e, z, col);
+          if (a.e.wide && col + 16 <= a.e.N) {
+            if (lane < rows) ln_store16(a.e, z, m0 + row, col);
+          } else {
+            ln_store_turned(a.e, z, turn, m0 + 32 * quad, rows, col, min(16, a.e.N - col), lane);
           }
         }
       }
-      __syncwarp();
-      tc_fence_before();
-      if (lane == 0) mbar_arrive(&S.tempty[b]);
-      if (a.split > 1) {
-        __threadfence();
-        named_bar_sync(1, 32 * kLnEpiWarps);
-        if (etid == 0) {
-          __threadfence();
-          S.last = atomicAdd(a.arrived + t.tile, 1u) == static_cast<uint32_t>(a.split) - 1u;
-          __threadfence();
-        }
-        named_bar_sync(1, 32 * kLnEpiWarps);
-        if (S.last) {
-          __threadfence();
-          if (etid == 0) a.arrived[t.tile] = 0u;
-          const size_t each = static_cast<size_t>(a.tile_n) * a.rows;
-          const float* from = a.partial + static_cast<size_t>(t.tile) * a.split * each + row;
-          if (row < a.rows && m < a.e.M)
-            for (int c = 16 * half; c < a.tile_n && n0 + c < a.e.N; c += 32) {
-              float z[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-#pragma unroll 2
-              for (int s = 0; s < a.split; ++s)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  z[i] = __fadd_rn(z[i], __ldcg(from + s * each + static_cast<size_t>(c + i) * a.rows));
-              ln_store16(a.e, z, m, n0 + c);
-            }
-        }
-      }
+      release();
     }
     if (!ok && lane == 0) {
       atomicOr(a.err, kErrRingWait);
@@ -467,7 +688,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
+  if (warp == 9) tmem_dealloc(tmem, a.tmem_cols);
 }
 
 // ---------------------------------------------------------------- host side
@@ -485,35 +706,63 @@ static PFN_cuTensorMapEncodeTiled_v12000 ln_encode_fn() {
   return fn;
 }
 
-// BF16 tensor [rows, cols] with row stride ld, box box_rows x 64 values, 128-byte swizzle, zeros outside.
-static bool ln_map(CUtensorMap* map, const void* base, int rows, int cols, long long ld, int box_rows) {
+// BF16 tensor [rows, cols] with row stride ld, 128-byte swizzle, zeros outside. slices = 0: box box_rows x 64 values; else
+// the whole 64-value blocks of its rows as a third dimension, box 64 values x box_rows x slices.
+static bool ln_map(CUtensorMap* map, const void* base, int rows, int cols, long long ld, int box_rows, int slices) {
   auto fn = ln_encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  cuuint32_t box[2] = {kLnKBlock, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint64_t n = static_cast<cuuint64_t>(rows), pitch = static_cast<cuuint64_t>(ld) * 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), n, 0};
+  cuuint64_t strides[2] = {pitch, 128};
+  cuuint32_t box[3] = {kLnKBlock, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(slices)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (slices > 0) {
+    dims[0] = kLnKBlock;
+    dims[2] = static_cast<cuuint64_t>(cols / kLnKBlock);
+  }
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, slices > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product of more than kLnRowsMax tokens is cut.
+// Whether a product goes to the kernels of few tokens. Measured with the weights out of L2, they against tiles: 8 tokens of
+// 256 x 7168 4.6 us / 11.1, of 7168 x 2048 8.2 / 10.3, of 4096 x 7168 12.6 / 30; 16 tokens of 256 x 7168 5.7 / 10.1, of
+// 1500 x 2664 6.6 / 9.3, of 7168 x 2048 14.3 / 10.3, of 4096 x 7168 22.8 / 21.9.
+static bool ln_few(int M, int N, int K) {
+  return M <= 8 || (M <= kLnFewMax && static_cast<long long>(N) * K <= (1 << 23));
+}
+
+// How a product in tiles is cut: by what the ways cost, in clocks, to within 2 % of the best way of 25 shapes that were
+// swept (tokens 16 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block takes its bytes at 78 a clock (tokens and weights
+// arrive through one port), 385 clocks at least; a tile's epilogue 4000 for 256 columns, hidden behind the next tile's
+// products but for the last one's; cutting K 10,500 and the partial sums' way through L2.
 struct LnPlan {
-  int tile_n, tiles_m, tiles_n, blocks, split, rows;
+  int tile_m, tile_n, tiles_m, tiles_n, blocks, split;
 };
 static LnPlan ln_plan(int M, int N, int K, int sms) {
   LnPlan p;
-  p.rows = M < 128 ? M : 128;
-  p.tiles_m = (M + 127) / 128;
   p.blocks = (K + kLnKBlock - 1) / kLnKBlock;
-  p.tile_n = N < 256 ? (N + 15) / 16 * 16 : 256;
-  p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
-  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  p.split = 1;
-  if (tiles < sms) {
-    p.split = sms / static_cast<int>(tiles);
-    if (p.split > p.blocks) p.split = p.blocks;
+  p.tiles_m = (M + 127) / 128;
+  p.tile_m = p.tiles_m == 1 ? M : ((M + p.tiles_m - 1) / p.tiles_m + 7) / 8 * 8;
+  p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
+  const int box_m = (p.tile_m + 7) / 8 * 8;
+  long long best = -1;
+  for (int tile_n = 16; tile_n <= 256 && tile_n < N + 16; tile_n += 16) {
+    const int tiles_n = (N + tile_n - 1) / tile_n;
+    const long long tiles = static_cast<long long>(p.tiles_m) * tiles_n;
+    const long long bytes = (box_m + tile_n) * 128ll, part = static_cast<long long>(p.tile_m) * tile_n * 4;
+    const long long block = bytes / 78 > 385 ? bytes / 78 : 385, finish = 4000ll * tile_n / 256;
+    for (int split = 1; split <= 16 && split <= p.blocks && (split == 1 || tiles * split <= sms); ++split) {
+      const long long waves = (tiles * split + sms - 1) / sms, main = (p.blocks + split - 1) / split * block;
+      long long cost = waves * (main > finish ? main : finish) + finish;
+      if (split > 1) cost += 10500 + part / 122 + split * part / 11;
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.tile_n = tile_n;
+        p.tiles_n = tiles_n;
+        p.split = split;
+      }
+    }
   }
   return p;
 }
@@ -525,13 +774,13 @@ static int ln_sms(int dev) {
 
 // Powers of two where K is cut, so that a program's products need few sizes.
 size_t linear_workspace_bytes(int M, int N, int K) {
-  if (M <= kLnRowsMax) return kLnHeader;
+  if (ln_few(M, N, K)) return kLnHeader;
   int dev = 0, sms = -1;
   if (cudaGetDevice(&dev) == cudaSuccess) sms = ln_sms(dev);
   const LnPlan p = ln_plan(M, N, K, sms > 0 ? sms : 152);
   if (p.split == 1) return kLnHeader;
   const size_t need =
-      kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * p.rows * sizeof(float);
+      kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * p.tile_m * sizeof(float);
   size_t bytes = 65536;
   while (bytes < need) bytes *= 2;
   return bytes;
@@ -549,8 +798,9 @@ static LnEpilogue ln_epilogue(const Linear& l) {
   e.M = l.M;
   e.N = l.N;
   const long long size = l.out_f32 ? 4 : 2;
-  e.wide = reinterpret_cast<uintptr_t>(l.out) % 32 == 0 && l.ldo * size % 32 == 0 &&
-           (l.residual == nullptr || (reinterpret_cast<uintptr_t>(l.residual) % 32 == 0 && l.ldr * size % 32 == 0));
+  const long long any = static_cast<long long>(reinterpret_cast<uintptr_t>(l.out)) | l.ldo * size |
+                        (l.residual != nullptr ? static_cast<long long>(reinterpret_cast<uintptr_t>(l.residual)) | l.ldr * size : 0);
+  e.wide = any % 32 == 0 ? 32 : any % 16 == 0 ? 16 : 0;
   return e;
 }
 
@@ -571,7 +821,7 @@ static int ln_launch(const void* kernel, int grid, int threads, size_t smem, voi
   return FME_OK;
 }
 
-static int linear_rows(const Linear& l, int sms, cudaStream_t st) {
+static int linear_few(const Linear& l, int sms, cudaStream_t st) {
   LnRowsArgs a = {};
   a.x = static_cast<const __nv_bfloat16*>(l.x);
   a.w = static_cast<const __nv_bfloat16*>(l.w);
@@ -579,16 +829,20 @@ static int linear_rows(const Linear& l, int sms, cudaStream_t st) {
   a.ldw = l.ldw;
   a.K = l.K;
   a.e = ln_epilogue(l);
-  // More warps a row while there are fewer than 16 an SM and each keeps 32 chunks.
-  const int pairs = (l.N + kLnRows - 1) / kLnRows;
+  // More warps share a row's K range while there are fewer than 16 warps an SM and each keeps two loads a lane.
   a.share = 1;
-  while (a.share < kLnRowWarps && pairs * a.share < 16 * sms && l.K >= 512 * a.share) a.share *= 2;
-  const int groups = kLnRowWarps / a.share;
-  void (*kernel)(LnRowsArgs) = l.M == 1   ? linear_rows_kernel<1>
-                               : l.M == 2 ? linear_rows_kernel<2>
-                               : l.M <= 4 ? linear_rows_kernel<4>
-                                          : linear_rows_kernel<8>;
-  return ln_launch(reinterpret_cast<const void*>(kernel), (pairs + groups - 1) / groups, 32 * kLnRowWarps, 0, &a, st);
+  if (l.M == 1) {
+    const int pairs = (l.N + kLnRows - 1) / kLnRows;
+    while (a.share < kLnRowWarps && pairs * a.share < 16 * sms && l.K >= 512 * a.share) a.share *= 2;
+    const int groups = kLnRowWarps / a.share;
+    return ln_launch(reinterpret_cast<const void*>(linear_one_kernel), (pairs + groups - 1) / groups, 32 * kLnRowWarps, 0,
+                     &a, st);
+  }
+  const int rows8 = (l.N + 7) / 8;
+  while (a.share < kLnFewWarps && rows8 * a.share < 16 * sms && l.K >= 64 * a.share) a.share *= 2;
+  const int groups = kLnFewWarps / a.share;
+  return ln_launch(reinterpret_cast<const void*>(l.M > 8 ? linear_few_kernel<true> : linear_few_kernel<false>),
+                   (rows8 + groups - 1) / groups, 32 * kLnFewWarps, 0, &a, st);
 }
 
 int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_t st) {
@@ -600,30 +854,47 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   if (cudaGetDevice(&dev) != cudaSuccess) return set_last_error(FME_ECUDA, "cudaGetDevice failed");
   const int sms = ln_sms(dev);
   if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
-  if (l.M <= kLnRowsMax) return linear_rows(l, sms, st);
+  if (ln_few(l.M, l.N, l.K)) return linear_few(l, sms, st);
   const LnPlan p = ln_plan(l.M, l.N, l.K, sms);
   LnTcArgs a = {};
   a.e = ln_epilogue(l);
-  a.rows = p.rows;
-  a.box_m = (p.rows + 7) / 8 * 8;
+  a.rows = p.tile_m;
+  a.tile_m = p.tile_m;
+  a.box_m = (p.tile_m + 7) / 8 * 8;
   a.tiles_m = p.tiles_m;
   a.tiles_n = p.tiles_n;
   a.tile_n = p.tile_n;
   a.blocks = p.blocks;
-  a.split = p.split;
-  a.units = p.tiles_m * p.tiles_n * p.split;
-  const int stage = kLnABytes + a.tile_n * 128;
-  a.stages = kLnRingBytes / stage < kLnMaxStages ? kLnRingBytes / stage : kLnMaxStages;
+  const int block = (a.box_m + a.tile_n) * 128;  // bytes of a K block
+  a.slices = kLnStageBytes / block;
+  if (a.slices < 4 && 8 * block <= kLnRingBytes) a.slices = 4;
+  if (a.slices > 8) a.slices = 8;
+  if (a.slices > p.blocks) a.slices = p.blocks;
+  a.groups = (p.blocks + a.slices - 1) / a.slices;
+  // A box of several blocks cannot end inside one.
+  a.single = a.slices == 1 ? 0 : l.K % kLnKBlock == 0 ? a.groups : a.groups - 1;
+  a.chunk = l.out_f32 ? (kLnChunk + a.slices - 1) / a.slices : a.groups;
+  a.split = p.split < a.groups ? p.split : a.groups;
+  a.units = p.tiles_m * p.tiles_n * a.split;
+  a.stages = kLnRingBytes / (a.slices * block);
+  if (a.stages > kLnMaxStages) a.stages = kLnMaxStages;
   a.tmem_cols = 32;
   while (a.tmem_cols < 2u * a.tile_n) a.tmem_cols *= 2;
-  if (!ln_map(&a.mapx, l.x, l.M, l.K, l.ldx, a.box_m) || !ln_map(&a.mapw, l.w, l.N, l.K, l.ldw, a.tile_n))
+  if (!ln_map(&a.mapx1, l.x, l.M, l.K, l.ldx, a.box_m, 0) || !ln_map(&a.mapw1, l.w, l.N, l.K, l.ldw, a.tile_n, 0) ||
+      (l.K >= kLnKBlock && (!ln_map(&a.mapx, l.x, l.M, l.K, l.ldx, a.box_m, a.slices) ||
+                            !ln_map(&a.mapw, l.w, l.N, l.K, l.ldw, a.tile_n, a.slices))))
     return set_last_error(FME_ECUDA, "cuTensorMapEncodeTiled failed or unavailable");
+  if (l.K < kLnKBlock) {  // no whole block: never loaded from
+    a.mapx = a.mapx1;
+    a.mapw = a.mapw1;
+  }
   a.err = static_cast<uint32_t*>(workspace);
   a.arrived = a.err + 64;
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kLnHeader);
   a.timeout_ns = wait_timeout_ns();
-  if (!ensure_smem_attr(dev, reinterpret_cast<const void*>(linear_tc_kernel), kLnSmemBytes)) return FME_ECUDA;
-  return ln_launch(reinterpret_cast<const void*>(linear_tc_kernel), a.units < sms ? a.units : sms, kLnThreads,
+  const void* kernel = reinterpret_cast<const void*>(a.chunk < a.groups ? linear_tc_kernel<true> : linear_tc_kernel<false>);
+  if (!ensure_smem_attr(dev, kernel, kLnSmemBytes)) return FME_ECUDA;
+  return ln_launch(kernel, a.units < sms ? a.units : sms, kLnThreads,
                    kLnSmemBytes, &a, st);
 }
 
