@@ -43,7 +43,8 @@ struct LnEpilogue {
   long long ldr, ldo;
   void* out;
   int act, out_f32;
-  int wide;  // bytes that out (and residual) rows start at multiples of, where those are 32 or 16
+  int bias16;  // bias is 16-byte aligned
+  int wide;    // bytes that out (and residual) rows start at multiples of, where those are 32 or 16
   int M, N;
 };
 
@@ -106,102 +107,149 @@ __device__ __forceinline__ uint32_t ln_bf16x2(float lo, float hi) {
   return r;
 }
 
-// ln_act for outputs of 8 bits' precision: exp and reciprocal by the hardware's approximations (a few 2^-22).
+// For outputs of 8 bits' precision: the hardware's approximate reciprocal (a few 2^-23).
 __device__ __forceinline__ float ln_recip_approx(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
-__device__ __forceinline__ float ln_act_bf16(float z, int act) {
-  switch (act) {
-    case FME_ACT_SILU:
-      return __fmul_rn(z, ln_recip_approx(__fadd_rn(1.0f, __expf(-z))));
-    case FME_ACT_SIGMOID:
-      return ln_recip_approx(__fadd_rn(1.0f, __expf(-z)));
-    default:
-      return ln_act(z, act);
-  }
-}
 
-// Sixteen sums of one row, columns n .. n + 15 (bias and activation).
+// Sixteen sums of one row, columns n .. n + 15: bias and activation. (The cases stand outside the loops: inside them each
+// value's code holds every case's.) BF16 outputs take exp and reciprocal by the hardware's approximations.
 __device__ __forceinline__ void ln_finish16(const LnEpilogue& e, float (&z)[16], int n) {
-  if (e.bias != nullptr) {
+  if (e.bias != nullptr && e.bias16 && n + 16 <= e.N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(e.bias + n) + i);
+      z[4 * i] = __fadd_rn(z[4 * i], b.x);
+      z[4 * i + 1] = __fadd_rn(z[4 * i + 1], b.y);
+      z[4 * i + 2] = __fadd_rn(z[4 * i + 2], b.z);
+      z[4 * i + 3] = __fadd_rn(z[4 * i + 3], b.w);
+    }
+  } else if (e.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], n + i < e.N ? __ldg(e.bias + n + i) : 0.0f);
   }
   if (e.act == FME_ACT_NONE) return;
-  if (e.out_f32) {
+  if (e.act == FME_ACT_SILU && !e.out_f32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], e.act);
+    for (int i = 0; i < 16; ++i) z[i] = __fmul_rn(z[i], ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i]))));
+  } else if (e.act == FME_ACT_SIGMOID && !e.out_f32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i])));
+  } else if (e.act == FME_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_RELU);
+  } else if (e.act == FME_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_SILU);
+  } else if (e.act == FME_ACT_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_SIGMOID);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = ln_act_bf16(z[i], e.act);
+    for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_GELU);
   }
 }
 
-// Adds the residual to sixteen values of one row and stores them, 32 or 16 bytes at a time.
-__device__ __forceinline__ void ln_store16(const LnEpilogue& e, float (&z)[16], int row, int n) {
-  const size_t r = static_cast<size_t>(row) * e.ldr + n, o = static_cast<size_t>(row) * e.ldo + n;
-  const bool sector = e.wide == 32;
-  uint32_t w[8];
-  if (e.out_f32) {
+// A chunk is sixteen columns (n .. n + 15, the first `cols` of them) of a warp's 32 rows (from `row`, the first `rows` of
+// them). Whole chunks of rows that start at multiples of 16 bytes are stored as the accumulator gives them, a lane a row, 32
+// or 16 bytes at a time. Others are turned through shared memory, so that neighbouring lanes store neighbouring values
+// (1533 x 895 x 3584: 16.4 us; a lane a row, value by value, 41.7).
+struct LnChunk {
+  int row, rows, n, cols;
+  bool whole;
+};
+// The residual of a chunk, asked for before its sums are read: bits of the values this lane stores.
+__device__ __forceinline__ void ln_residual(const LnEpilogue& e, const LnChunk& c, int lane, uint32_t (&raw)[16]) {
+  if (e.residual == nullptr) return;
+  if (c.whole) {
+    if (lane >= c.rows) return;
+    const size_t at = static_cast<size_t>(c.row + lane) * e.ldr + c.n;
+    uint32_t w[8];
+    if (e.out_f32) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h) {
+        ln_ld32(static_cast<const float*>(e.residual) + at + 8 * h, w, e.wide == 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[8 * h + i] = w[i];
+      }
+    } else {
+      ln_ld32(static_cast<const __nv_bfloat16*>(e.residual) + at, w, e.wide == 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = w[i];
+    }
+  } else if ((lane & 15) < c.cols) {
+    const int r0 = lane >> 4;
+    const size_t at = static_cast<size_t>(c.row + r0) * e.ldr + c.n + (lane & 15);
+    if (e.out_f32) {
+      const float* from = static_cast<const float*>(e.residual) + at;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i + r0 < c.rows) raw[i] = __float_as_uint(from[2 * i * e.ldr]);
+    } else {
+      const uint16_t* from = static_cast<const uint16_t*>(e.residual) + at;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i + r0 < c.rows) raw[i] = from[2 * i * e.ldr];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) raw[i] <<= 16;
+    }
+  }
+}
+// Adds the residual to a chunk and stores it. z: the sums of row `lane`.
+__device__ __forceinline__ void ln_store_chunk(const LnEpilogue& e, const LnChunk& c, float (&z)[16],
+                                               const uint32_t (&raw)[16], float* turn, int lane) {
+  if (c.whole) {
+    if (lane >= c.rows) return;
+    const size_t at = static_cast<size_t>(c.row + lane) * e.ldo + c.n;
+    const bool sector = e.wide == 32;
+    uint32_t w[8];
+    if (e.out_f32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = __float_as_uint(e.residual != nullptr ? __fadd_rn(z[8 * h + i], __uint_as_float(raw[8 * h + i]))
+                                                       : z[8 * h + i]);
+        ln_st32(static_cast<float*>(e.out) + at + 8 * h, w, sector);
+      }
+    } else {
       if (e.residual != nullptr) {
-        ln_ld32(static_cast<const float*>(e.residual) + r + 8 * h, w, sector);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[8 * h + i] = __fadd_rn(z[8 * h + i], __uint_as_float(w[i]));
+        for (int i = 0; i < 8; ++i) {
+          z[2 * i] = __fadd_rn(z[2 * i], __uint_as_float(raw[i] << 16));
+          z[2 * i + 1] = __fadd_rn(z[2 * i + 1], __uint_as_float(raw[i] & 0xFFFF0000u));
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z[8 * h + i]);
-      ln_st32(static_cast<float*>(e.out) + o + 8 * h, w, sector);
+      for (int i = 0; i < 8; ++i) w[i] = ln_bf16x2(z[2 * i], z[2 * i + 1]);
+      ln_st32(static_cast<__nv_bfloat16*>(e.out) + at, w, sector);
     }
-  } else {
-    if (e.residual != nullptr) {
-      ln_ld32(static_cast<const __nv_bfloat16*>(e.residual) + r, w, sector);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z[2 * i] = __fadd_rn(z[2 * i], __uint_as_float(w[i] << 16));
-        z[2 * i + 1] = __fadd_rn(z[2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = ln_bf16x2(z[2 * i], z[2 * i + 1]);
-    ln_st32(static_cast<__nv_bfloat16*>(e.out) + o, w, sector);
+    return;
   }
-}
-
-// The same for a warp's 32 rows (from `row`, the first `rows` of them) whose starts do not suit whole sectors, or of which
-// only the first `cols` columns exist: turned through shared memory, so that neighbouring lanes store neighbouring
-// values (1533 x 895 outputs: see linear_tc_kernel).
-__device__ __forceinline__ void ln_store_turned(const LnEpilogue& e, const float (&z)[16], float* turn, int row, int rows,
-                                                int n, int cols, int lane) {
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 16; ++i) turn[lane * 17 + i] = z[i];
   __syncwarp();
   const int col = lane & 15, r0 = lane >> 4;
-  if (col >= cols) return;
+  if (col >= c.cols) return;
   // All loads before the first store: the compiler cannot know that they do not meet.
-  float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = turn[(2 * i + r0) * 17 + col];
-  const size_t from = static_cast<size_t>(row + r0) * e.ldr + n + col, to = static_cast<size_t>(row + r0) * e.ldo + n + col;
+  for (int i = 0; i < 16; ++i) z[i] = turn[(2 * i + r0) * 17 + col];
   if (e.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (2 * i + r0 < rows)
-        v[i] = __fadd_rn(v[i], e.out_f32 ? static_cast<const float*>(e.residual)[from + 2 * i * e.ldr]
-                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[from + 2 * i * e.ldr]));
+    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], __uint_as_float(raw[i]));
   }
+  const size_t at = static_cast<size_t>(c.row + r0) * e.ldo + c.n + col;
   if (e.out_f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (2 * i + r0 < rows) static_cast<float*>(e.out)[to + 2 * i * e.ldo] = v[i];
+      if (2 * i + r0 < c.rows) static_cast<float*>(e.out)[at + 2 * i * e.ldo] = z[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (2 * i + r0 < rows) static_cast<__nv_bfloat16*>(e.out)[to + 2 * i * e.ldo] = __float2bfloat16_rn(v[i]);
+      if (2 * i + r0 < c.rows) static_cast<__nv_bfloat16*>(e.out)[at + 2 * i * e.ldo] = __float2bfloat16_rn(z[i]);
   }
 }
 
@@ -592,6 +640,17 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&S.tempty[n & 1]);
         ++n;
       };
+      // This thread's column chunks: 32 i + 16 half.
+      auto chunk = [&](int c) {
+        LnChunk k;
+        k.row = m0 + 32 * quad;
+        k.rows = rows;
+        k.n = n0 + c + 16 * half;
+        k.cols = min(16, a.e.N - k.n);
+        k.whole = a.e.wide != 0 && k.cols == 16;
+        return k;
+      };
+      auto has = [&](int c) { return c + 16 * half < a.tile_n && n0 + c + 16 * half < a.e.N; };
       if (CHUNKED) {
         // The accumulations' sums meet in registers, 16 columns 32 i + 16 half each; the tile's go back over the last one's.
         float z[8][16];
@@ -651,30 +710,27 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         __threadfence();
       }
       if (mine && rows > 0) {
-        for (int c = 0; c + 16 * half < a.tile_n; c += 32) {
-          const int col = n0 + c + 16 * half;
+        for (int c = 0; has(c); c += 32) {
+          const LnChunk k = chunk(c);
+          uint32_t raw[16];
+          ln_residual(a.e, k, lane, raw);
           float z[16];
           if (a.split == 1) {
             tmem_ld_issue(base + c, z);
             tmem_ld_join(z);
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) z[k] = 0.0f;
+            for (int i = 0; i < 16; ++i) z[i] = 0.0f;
             if (row < a.rows) {
               const float* from = tile + c * a.rows;
 #pragma unroll 4
               for (int s = 0; s < a.split; ++s)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) z[k] = __fadd_rn(z[k], __ldcg(from + s * each + k * a.rows));
+                for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], __ldcg(from + s * each + i * a.rows));
             }
           }
-          if (col >= a.e.N) break;
-          ln_finish16(a.e, z, col);
-          if (a.e.wide && col + 16 <= a.e.N) {
-            if (lane < rows) ln_store16(a.e, z, m0 + row, col);
-          } else {
-            ln_store_turned(a.e, z, turn, m0 + 32 * quad, rows, col, min(16, a.e.N - col), lane);
-          }
+          ln_finish16(a.e, z, k.n);
+          ln_store_chunk(a.e, k, z, raw, turn, lane);
         }
       }
       release();
@@ -789,6 +845,7 @@ size_t linear_workspace_bytes(int M, int N, int K) {
 static LnEpilogue ln_epilogue(const Linear& l) {
   LnEpilogue e = {};
   e.bias = l.bias;
+  e.bias16 = reinterpret_cast<uintptr_t>(l.bias) % 16 == 0;
   e.residual = l.residual;
   e.ldr = l.ldr;
   e.ldo = l.ldo;
