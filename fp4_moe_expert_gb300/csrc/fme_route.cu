@@ -188,27 +188,49 @@ __device__ __forceinline__ float rt_from_key(uint32_t k) {
 template <int J>
 __device__ __forceinline__ uint32_t rt_groups(const RtArgs& a, const uint32_t (&gk)[J], int lane) {
   uint32_t mine = 0u;  // lane g: group g's sum, as a key
-#pragma unroll 1
-  for (int g = 0; g < a.groups; ++g) {
-    const int lo = g * a.group_size, hi = lo + a.group_size;
+  auto sum_of = [&](uint32_t first, uint32_t second) {
+    return a.group_top == 1 ? first : max(1u, ordered_key(__fadd_rn(rt_from_key(first), rt_from_key(second))));
+  };
+  if (a.group_size % J == 0) {
+    // A lane's experts are of one group, and a group those of `seg` lanes: a tree over them.
+    const int seg = a.group_size / J, at = lane % seg;
     uint32_t first = 0u, second = 0u;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const uint32_t k = J * lane + j >= lo && J * lane + j < hi ? gk[j] : 0u;
-      second = max(second, min(first, k));
-      first = max(first, k);
+      second = max(second, min(first, gk[j]));
+      first = max(first, gk[j]);
     }
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, first);
-    uint32_t sum = top;
-    if (a.group_top == 2) {
-      const int win = __ffs(__ballot_sync(0xFFFFFFFFu, first == top)) - 1;
-      const uint32_t next = __reduce_max_sync(0xFFFFFFFFu, lane == win ? second : first);
-      sum = max(1u, ordered_key(__fadd_rn(rt_from_key(top), rt_from_key(next))));
+    for (int d = 1; d < seg; d <<= 1) {
+      const uint32_t f = __shfl_down_sync(0xFFFFFFFFu, first, d), s = __shfl_down_sync(0xFFFFFFFFu, second, d);
+      if (at + d < seg) {
+        second = max(min(first, f), max(second, s));
+        first = max(first, f);
+      }
     }
-    if (lane == g) mine = sum;
+    mine = __shfl_sync(0xFFFFFFFFu, sum_of(first, second), lane * seg & 31);
+    if (lane >= a.groups) mine = 0u;
+  } else {
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+      const int lo = g * a.group_size, hi = lo + a.group_size;
+      uint32_t first = 0u, second = 0u;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint32_t k = J * lane + j >= lo && J * lane + j < hi ? gk[j] : 0u;
+        second = max(second, min(first, k));
+        first = max(first, k);
+      }
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, first);
+      uint32_t next = 0u;
+      if (a.group_top == 2) {
+        const int win = __ffs(__ballot_sync(0xFFFFFFFFu, first == top)) - 1;
+        next = __reduce_max_sync(0xFFFFFFFFu, lane == win ? second : first);
+      }
+      if (lane == g) mine = sum_of(top, next);
+    }
   }
   int rank = 0;
-#pragma unroll 1
+#pragma unroll 8
   for (int g = 0; g < a.groups; ++g) {
     const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine, g);
     rank += k > mine || (k == mine && g < lane);
