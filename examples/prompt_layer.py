@@ -38,7 +38,7 @@ def shared_expert(xq, sx, w13, s13, w2, s2):
 def prompt_layer(x, residual, gamma, router, bias, routed, shared):
     """(layer output [T, H], new residual [T, H], normed [T, H], router logits) of a prompt x [T, H]."""
     xq, sx, residual, normed = fme.add_rmsnorm_fp8(x, gamma, residual, EPS, want_normed=True)
-    logits = normed @ router
+    logits = fme.linear_bf16(normed, router, out_dtype=torch.float32)
     y, _, _ = fme.moe_prompt_fp8(xq, sx, logits, bias, *routed, TOP_K, LIMIT, SCALE, False,
                                  shared_out=shared_expert(xq, sx, *shared))
     return y, residual, normed, logits
@@ -52,7 +52,7 @@ def main():
     x = torch.randn(T, H, device="cuda").bfloat16()
     residual = (3 * torch.randn(T, H, device="cuda")).bfloat16()
     gamma = (1 + 0.1 * torch.randn(H, device="cuda")).bfloat16()
-    router = (torch.randn(H, E, device="cuda") / H ** 0.5).bfloat16()
+    router = (torch.randn(E, H, device="cuda") / H ** 0.5).bfloat16()
     bias = 0.05 * torch.randn(E, device="cuda")
     routed = (*fp8_weights(E, 2 * I, H), *fp8_weights(E, H, I))
     shared = (*fp8_weights(1, 2 * I, H), *fp8_weights(1, H, I))

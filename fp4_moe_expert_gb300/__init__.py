@@ -744,15 +744,7 @@ def moe_prompt_workspaces(T, H, I, E, top_k, device):
             Workspace(moe_grouped_fp8_workspace(R, I, H, E), device))
 
 
-def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, shared_out=None,
-                   workspaces=None):
-    """The routed FP8 experts of a prompt of T tokens, combined: moe_route, moe_grouped_swiglu_fp8 on the tokens' rows,
-    moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
-
-    xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
-    weights these are, and whose shapes are checked alike. Returns (y [T, H] BF16, ids, weights); no tokens give empty
-    ones. Without workspaces (moe_prompt_workspaces) the binding's kept ones serve, whose device errors
-    kept_workspace_error reads; a graph that is to report its errors needs workspaces of the caller's."""
+def _need_prompt(xq, sx, logits, bias, w13, w2, shared_out=None):
     T, H = xq.shape
     E, I = logits.shape[-1], w2.shape[-1]
     for t, shape, name in ((sx, (T, H // 128), "sx"), (logits, (T, E), "logits"), (bias, (E,), "bias"),
@@ -761,14 +753,63 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
             raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
         if t is not None and t.device != xq.device:
             raise ValueError(f"{name}: on {t.device}, the other operands on {xq.device}")
+
+
+def moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, workspaces=None,
+                        score="sigmoid", groups=1, top_groups=None, group_top=None, renormalise=True):
+    """The routed FP8 experts of a prompt of T tokens before their combination: routing, moe_grouped_swiglu_fp8 on the
+    tokens' rows and moe_grouped_gemm_fp8 back to route order. Arguments as moe_prompt_fp8. Returns (out [T * top_k, H]
+    BF16 unweighted route rows, ids, weights), which moe_finalize or block_norm combine."""
+    _need_prompt(xq, sx, logits, bias, w13, w2)
     ws = workspaces or (None, None, None)
-    ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale, workspace=ws[0])
+    if (score, groups, renormalise) == ("sigmoid", 1, True) and bias is not None:
+        if top_groups not in (None, 1):
+            raise ValueError(f"top_groups={top_groups} of one group")
+        ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale, workspace=ws[0])
+    else:
+        ids, weights, offsets, rows, tokens = moe_route_groups(logits, bias, top_k, score, groups, top_groups, group_top,
+                                                               renormalise, scale, workspace=ws[0])
     hq, sh = moe_grouped_swiglu_fp8(xq, sx, w13, s13, offsets, in_rows=tokens, limit=limit, ue8m0=ue8m0,
                                     workspace=ws[1])
     out = moe_grouped_gemm_fp8(hq, sh, w2, s2, offsets, out_rows=rows, workspace=ws[2])
+    return out, ids, weights
+
+
+def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, shared_out=None,
+                   workspaces=None, score="sigmoid", groups=1, top_groups=None, group_top=None, renormalise=True):
+    """The routed FP8 experts of a prompt of T tokens, combined: moe_route, moe_grouped_swiglu_fp8 on the tokens' rows,
+    moe_grouped_gemm_fp8 back to route order and moe_finalize (with shared_out [T, H] BF16 added when given).
+
+    xq [T, H] uint8 E4M3 and sx [T, H/128] float32 as add_rmsnorm_fp8 returns them; the rest as moe_routed_fp8, whose
+    weights these are, and whose shapes are checked alike. score, groups, top_groups, group_top and renormalise (and a
+    bias of None) ask for moe_route_groups' routing. Returns (y [T, H] BF16, ids, weights); no tokens give empty
+    ones. Without workspaces (moe_prompt_workspaces) the binding's kept ones serve, whose device errors
+    kept_workspace_error reads; a graph that is to report its errors needs workspaces of the caller's."""
+    _need_prompt(xq, sx, logits, bias, w13, w2, shared_out)
+    out, ids, weights = moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
+                                            workspaces, score, groups, top_groups, group_top, renormalise)
     if xq.shape[0] == 0:
         return out, ids, weights
     return moe_finalize(out, weights, shared_out), ids, weights
+
+
+def moe_prompt_block_fp8(xq, sx, normed, residual, router, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
+                         next_gamma=None, post_gamma=None, gate=None, residual_scale=1.0, eps=1e-5, quant=None,
+                         shared_out=None, workspaces=None, score="sigmoid", groups=1, top_groups=None, group_top=None,
+                         renormalise=True):
+    """A routed block of a prompt from the norm before it to the norm after it: linear_bf16 for the router's logits
+    (router [E, H] BF16, FP32 logits), the routed experts (moe_prompt_rows_fp8), and block_norm, which combines the
+    routes (shared_out [T, H] added), norms them with post_gamma, gates them, adds residual_scale * residual and norms
+    for the next block (next_gamma, quant).
+
+    xq, sx, normed [T, H] and residual [T, H] as add_rmsnorm_fp8 or block_norm return them (quant "fp8", with normed);
+    the rest as moe_prompt_fp8 and block_norm. Returns (q, scales, residual_out, normed, ids, weights): what the next
+    block takes (q, scales and normed None where not asked for: normed comes with next_gamma), and the routing."""
+    logits = linear_bf16(normed, router, out_dtype=torch.float32)
+    rows, ids, weights = moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
+                                             workspaces, score, groups, top_groups, group_top, renormalise)
+    return (*block_norm(rows, next_gamma, residual, weights, shared_out, post_gamma, gate, residual_scale, eps, quant,
+                        want_normed=next_gamma is not None), ids, weights)
 
 
 def moe_routed_nvfp4_workspace(M, H, N, L, top_k):

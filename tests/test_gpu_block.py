@@ -10,6 +10,8 @@ import torch
 from oracle import codecs, linear as oracle_linear, prompt, routing
 from oracle.ep_local import mx_exponent
 from oracle.finalize import finalize as oracle_finalize
+from oracle.routing import route_groups as routing_oracle
+from synth import workloads as W
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -314,11 +316,12 @@ def _check_norm(fme, d, quant, alpha, ue8m0=False, dev=None, **kw):
     h, y, dh, dy = prompt.block_norm(**d, residual_scale=alpha)
     q, s, res, normed = fme.block_norm(**(dev or _to_dev(d)), residual_scale=alpha, quant=quant, ue8m0=ue8m0,
                                        want_normed=True, **kw)
+    given = q, s, res, normed
     assert np.all(np.abs(_np(res) - h) <= dh + np.abs(h) * 2.0 ** -8 * 1.001)
     assert np.all(np.abs(_np(normed) - y) <= dy + np.abs(y) * 2.0 ** -8 * 1.001)
     if quant is None:
         assert q is None and s is None
-        return res, normed
+        return given
     if quant == "fp8":
         s = _np(s).astype(np.float64)
         base = np.maximum(np.abs(y).reshape(T, H // 128, 128).max(-1), 1e-10) / 448
@@ -337,7 +340,7 @@ def _check_norm(fme, d, quant, alpha, ue8m0=False, dev=None, **kw):
         assert np.all((e >= low) & (e <= high))
         s = np.repeat(np.exp2(e.astype(np.float64)), 32, axis=1)
     _check_codes(_np(q), s, y, dy + 4 * U * np.abs(y))
-    return q, s, res, normed
+    return given
 
 
 @pytest.mark.parametrize("quant", ["fp8", "mxfp8", None])
@@ -488,3 +491,61 @@ def test_streams_of_the_operators_share_nothing(fme):
     torch.cuda.synchronize()
     for r, runs in zip(ref, got):
         assert all(torch.equal(r, g) for g in runs)
+
+
+# --------------------------------------------------------------------------- together
+@pytest.mark.parametrize("T,routing", [(1, dict(groups=8, top_groups=4)), (90, dict(score="softmax", renormalise=False)),
+                                       (300, dict(groups=4, top_groups=2, group_top=1)), (40, dict())])
+def test_routed_block(fme, T, routing):
+    """A block from its norm to the next block's: each step against the oracle on the step before it, the whole equal to
+    the steps bit for bit."""
+    cfg = W.RAGGED
+    rng = np.random.default_rng(T)
+    w13h, w2h = W.fp8_weights_host(cfg, 61)
+    s13, s2 = W.fp8_weight_scales(cfg, 61)
+    experts = [_dev(v) for v in (w13h.full(), s13, w2h.full(), s2)]
+    x, r, g, pg = _bf(rng, T, cfg.H), _bf(rng, T, cfg.H), _bf(rng, cfg.H), _bf(rng, cfg.H)
+    router = codecs.bf16_round(_bf(rng, cfg.E, cfg.H) / np.float32(32))
+    bias = (0.1 * rng.normal(size=cfg.E)).astype(np.float32)
+    shared = _bf(rng, T, cfg.H)
+    dg, dpg, dsh, drouter, dbias = _dev(g, BF), _dev(pg, BF), _dev(shared, BF), _dev(router, BF), _dev(bias)
+    xq, sx, h, normed = fme.block_norm(_dev(x, BF), dg, _dev(r, BF), quant="fp8", want_normed=True)
+    args = (cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0)
+    got = fme.moe_prompt_block_fp8(xq, sx, normed, h, drouter, dbias, *experts, *args, next_gamma=dg, post_gamma=dpg,
+                                   gate=dpg, residual_scale=0.5, quant="fp8", shared_out=dsh, **routing)
+
+    logits = fme.linear_bf16(normed, drouter, out_dtype=torch.float32)
+    y, tol = oracle_linear.linear(_np(normed), router)
+    assert np.all(np.abs(_np(logits) - y) <= tol + U * np.abs(y))
+    rows, ids, weights = fme.moe_prompt_rows_fp8(xq, sx, logits, dbias, *experts, *args, **routing)
+    full = {"groups": 1, **routing}
+    full.setdefault("top_groups", full["groups"])
+    full.setdefault("group_top", 2)
+    rid, rw, gaps = routing_oracle(_np(logits), bias, cfg.top_k, scale=cfg.scale, **full)
+    sure = gaps > 32 * U
+    assert sure.mean() > 0.9 and np.array_equal(_np(ids)[sure], rid[sure])
+    assert np.all(np.abs(_np(weights) - rw)[sure] <= 80 * U * np.abs(rw)[sure])
+    d = dict(x=_np(rows), gamma=g, residual=_np(h), route_weights=_np(weights), shared_out=shared, post_gamma=pg, gate=pg)
+    dev = dict(x=rows, gamma=dg, residual=h, route_weights=weights, shared_out=dsh, post_gamma=dpg, gate=dpg)
+    last = _check_norm(fme, d, "fp8", 0.5, dev=dev)
+    for a, b in zip(got, (*last, ids, weights)):
+        assert torch.equal(a, b)
+    # The same routes combined by themselves.
+    y, pid, pw = fme.moe_prompt_fp8(xq, sx, logits, dbias, *experts, *args, shared_out=dsh, **routing)
+    assert torch.equal(pid, ids) and torch.equal(pw, weights)
+    assert torch.equal(y, fme.moe_finalize(rows, weights, dsh))
+
+
+def test_routed_block_without_tokens(fme):
+    cfg = W.RAGGED
+    w13h, w2h = W.fp8_weights_host(cfg, 62)
+    s13, s2 = W.fp8_weight_scales(cfg, 62)
+    experts = [_dev(v) for v in (w13h.full(), s13, w2h.full(), s2)]
+    g = torch.ones(cfg.H, dtype=BF, device=DEV)
+    none = torch.empty(0, cfg.H, dtype=BF, device=DEV)
+    xq, sx, h, normed = fme.block_norm(none, g, none, quant="fp8", want_normed=True)
+    got = fme.moe_prompt_block_fp8(xq, sx, normed, h, torch.zeros(cfg.E, cfg.H, dtype=BF, device=DEV), None, *experts,
+                                   cfg.top_k, cfg.limit, cfg.scale, cfg.ue8m0, next_gamma=g, quant="fp8", groups=4,
+                                   top_groups=2)
+    assert [tuple(t.shape) for t in got] == [(0, cfg.H), (0, cfg.H // 128), (0, cfg.H), (0, cfg.H), (0, cfg.top_k),
+                                             (0, cfg.top_k)]
