@@ -118,7 +118,7 @@ def _stream(device):
 def _need(t, dtype, shape, name, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, the other operands on {device}")
-    if t.dtype != dtype or t.shape != torch.Size(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} contiguous={t.is_contiguous()} cuda={t.is_cuda}")
 

@@ -701,8 +701,11 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         named_bar_sync(1, 32 * kLnEpiWarps);
         if (tid == 0) {
           __threadfence();
-          S.last = atomicAdd(a.arrived + t.tile, 1u) == static_cast<uint32_t>(a.split) - 1u;
+          const uint32_t before = atomicAdd(a.arrived + t.tile, 1u);
+          S.last = before == static_cast<uint32_t>(a.split) - 1u;
           if (S.last) a.arrived[t.tile] = 0u;
+          // A count that no call left: the tile may have no last unit, or one too early.
+          if (before >= static_cast<uint32_t>(a.split)) atomicOr(a.err, kErrCrossWait);
           __threadfence();
         }
         named_bar_sync(1, 32 * kLnEpiWarps);

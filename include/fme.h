@@ -592,7 +592,8 @@ int fme_block_norm(const void* x, long long ldx, const float* route_weights, int
  *   refused. The workspace (fme_linear_bf16_workspace) must be zeroed before
  *   its first use; it serves every product that needs no more. Errors:
  *   FME_OK, FME_EINVAL, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA; device waits
- *   that gave up set error bits 1 and 4 of the workspace.
+ *   that gave up set error bits 1 and 4 of the workspace, counters that no call
+ *   left (a workspace that was not cleared) bit 2.
  */
 int fme_linear_bf16(const void* x, long long ldx, const void* w, long long ldw, const float* bias, int activation,
                     const void* residual, long long ldr, int M, int N, int K, void* out, int out_dtype, long long ldo,
@@ -607,7 +608,7 @@ int fme_workspace_clear(void* workspace, size_t workspace_bytes, void* stream);
 /*
  * Read and clear the device error word of a workspace (synchronises stream).
  * *code receives 0 or a bit set: 1 = a ring wait timed out, 2 = a cross-CTA
- * wait timed out (fme_moe_route: or met counters that no call had left), 4 =
+ * wait timed out (fme_moe_route, fme_linear_bf16: or met counters that no call had left), 4 =
  * the producer could not drain its copies, 8 = a row index fell outside its
  * tensor or group offsets overlapped (the write was skipped). Returns
  * FME_ETIMEOUT when *code != 0, FME_OK otherwise.

@@ -108,6 +108,20 @@ def test_linear_is_the_same_bits_every_time(fme):
             assert torch.equal(ref, fme.linear_bf16(x, w, out_dtype=torch.float32))
 
 
+def test_linear_reports_a_workspace_that_was_not_cleared(fme):
+    M, N, K = 64, 256, 7168  # K is cut: units count their arrivals in the workspace
+    x, w = torch.randn(M, K, device=DEV).to(BF), torch.randn(N, K, device=DEV).to(BF)
+    ws = fme.Workspace(fme.linear_bf16_workspace(M, N, K), DEV)
+    assert ws.nbytes > 4096
+    ref = fme.linear_bf16(x, w, workspace=ws)
+    assert ws.error() == 0
+    ws.buf[256:4096] = 0x7F
+    fme.linear_bf16(x, w, workspace=ws)
+    assert ws.error() == 2
+    ws.clear()
+    assert torch.equal(fme.linear_bf16(x, w, workspace=ws), ref) and ws.error() == 0
+
+
 @pytest.mark.parametrize("M", [4, 70, 400])
 @pytest.mark.parametrize("f32", [False, True])
 def test_linear_strided_outputs(fme, M, f32):
