@@ -8,6 +8,7 @@ with ``python -m fp4_moe_expert_gb300.build`` or ``__graft_entry__.build()``).
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -418,10 +419,11 @@ def _launch_stream(device):
 
 def _rows(t, name):
     """Row stride of a BF16 CUDA matrix with contiguous rows."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != torch.bfloat16 or not t.is_cuda or (shape[1] > 1 and strides[1] != 1):
         raise ValueError(f"{name}: expected a CUDA bfloat16 matrix with contiguous rows, got {t.dtype} "
                          f"{tuple(t.shape)} strides={t.stride()} cuda={t.is_cuda}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8)
+    return strides[0] if shape[0] > 1 else max(shape[1], 8)
 
 
 def _out(t, shape, dtype, device, name):
@@ -552,6 +554,16 @@ def moe_route_groups(logits, bias, top_k, score="sigmoid", groups=1, top_groups=
 _QUANT = {None: 0, "fp8": 1, "mxfp8": 2}
 
 
+def _need_rows(t, shape, name, device):
+    """_rows of a matrix of this shape on this device."""
+    ld = _rows(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other operands on {device}")
+    return ld
+
+
 def block_norm(x, gamma, residual=None, route_weights=None, shared_out=None, post_gamma=None, gate=None,
                residual_scale=1.0, eps=1e-5, quant=None, ue8m0=False, want_normed=False, q=None, scales=None, normed=None,
                residual_out=None):
@@ -566,6 +578,7 @@ def block_norm(x, gamma, residual=None, route_weights=None, shared_out=None, pos
     ldx, dev = _rows(x, "x"), x.device
     n, H = x.shape
     T, top_k = n, 0
+    bf16, need_normed = torch.bfloat16, want_normed or normed is not None
     if quant not in _QUANT:
         raise ValueError(f"quant: expected one of {list(_QUANT)}, got {quant!r}")
     if route_weights is not None:
@@ -573,40 +586,35 @@ def block_norm(x, gamma, residual=None, route_weights=None, shared_out=None, pos
         _need(route_weights, torch.float32, (T, top_k), "route_weights", dev)
         if top_k == 0 or n != T * top_k:
             raise ValueError(f"x: expected {T} * {top_k} rows, got {n}")
-    if shared_out is not None:
-        if route_weights is None:
-            raise ValueError("shared_out without route_weights")
-        _need(shared_out, torch.bfloat16, (T, H), "shared_out", dev)
-    for v, name in ((gamma, "gamma"), (post_gamma, "post_gamma")):
-        if v is not None:
-            _need(v, torch.bfloat16, (H,), name, dev)
+        if shared_out is not None:
+            _need(shared_out, bf16, (T, H), "shared_out", dev)
+    elif shared_out is not None:
+        raise ValueError("shared_out without route_weights")
+    if gamma is not None:
+        _need(gamma, bf16, (H,), "gamma", dev)
+    elif quant is not None or need_normed:
+        raise ValueError("normed or quantised outputs without gamma")
+    if post_gamma is not None:
+        _need(post_gamma, bf16, (H,), "post_gamma", dev)
     ldg = ldr = 0
     if gate is not None:
-        if gate.device != dev:
-            raise ValueError(f"gate: on {gate.device}, the other operands on {dev}")
         if gate.dim() == 1:
-            _need(gate, torch.bfloat16, (H,), "gate", dev)
+            _need(gate, bf16, (H,), "gate", dev)
         else:
-            ldg = _rows(gate, "gate")
-            if gate.shape != (T, H):
-                raise ValueError(f"gate: expected {(H,)} or {(T, H)}, got {tuple(gate.shape)}")
+            ldg = _need_rows(gate, (T, H), "gate", dev)
     if residual is not None:
-        ldr = _rows(residual, "residual")
-        if residual.shape != (T, H):
-            raise ValueError(f"residual: expected {(T, H)}, got {tuple(residual.shape)}")
-        if residual.device != dev:
-            raise ValueError(f"residual: on {residual.device}, the other operands on {dev}")
-    if gamma is None and (quant is not None or want_normed or normed is not None):
-        raise ValueError("normed or quantised outputs without gamma")
+        ldr = _need_rows(residual, (T, H), "residual", dev)
     if quant is None and (q is not None or scales is not None):
         raise ValueError("q or scales without quant")
-    residual_out = _out(residual_out, (T, H), torch.bfloat16, dev, "residual_out")
-    if quant is not None:
-        mx = quant == "mxfp8"
+    residual_out = _out(residual_out, (T, H), bf16, dev, "residual_out")
+    if quant == "fp8":
         q = _out(q, (T, H), torch.uint8, dev, "q")
-        scales = _out(scales, (T, H // (32 if mx else 128)), torch.uint8 if mx else torch.float32, dev, "scales")
-    if want_normed or normed is not None:
-        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+        scales = _out(scales, (T, H // 128), torch.float32, dev, "scales")
+    elif quant is not None:
+        q = _out(q, (T, H), torch.uint8, dev, "q")
+        scales = _out(scales, (T, H // 32), torch.uint8, dev, "scales")
+    if need_normed:
+        normed = _out(normed, (T, H), bf16, dev, "normed")
     if T == 0:
         return q, scales, residual_out, normed
     _check(lib.fme_block_norm(x.data_ptr(), ldx, _addr(route_weights), top_k, _addr(shared_out), _addr(post_gamma),
@@ -625,10 +633,17 @@ def linear_bf16_workspace(M, N, K):
 
 def _stride(t, dtype, name, align=1):
     """Row stride of a CUDA matrix with contiguous rows; one row's, which nothing steps by, rounded up to `align`."""
-    if t.dtype != dtype or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != dtype or not t.is_cuda or (shape[1] > 1 and strides[1] != 1):
         raise ValueError(f"{name}: expected a CUDA {dtype} matrix with contiguous rows, got {t.dtype} {tuple(t.shape)} "
                          f"strides={t.stride()} cuda={t.is_cuda}")
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // align) * align
+    return strides[0] if shape[0] > 1 else -(-shape[1] // align) * align
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_bytes(current, M, N, K):
+    """linear_bf16_workspace on the current device (its index: sizes hang on the device's SMs)."""
+    return linear_bf16_workspace(M, N, K)
 
 
 def linear_bf16(x, w, bias=None, activation=None, residual=None, out_dtype=None, out=None, workspace=None):
@@ -665,7 +680,7 @@ def linear_bf16(x, w, bias=None, activation=None, residual=None, out_dtype=None,
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     if M == 0:
         return out
-    ws = _stream_workspace(linear_bf16_workspace(M, N, K), dev, workspace)
+    ws = _stream_workspace(_linear_bytes(torch.cuda.current_device(), M, N, K), dev, workspace)
     _check(lib.fme_linear_bf16(x.data_ptr(), ldx, w.data_ptr(), ldw, _addr(bias), _ACTIVATIONS[activation],
                                _addr(residual), ldr, M, N, K, out.data_ptr(), int(out_dtype == torch.bfloat16), ldo,
                                ws.buf.data_ptr(), ws.nbytes, _launch_stream(dev)))
