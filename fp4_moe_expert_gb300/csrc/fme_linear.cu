@@ -21,12 +21,15 @@
 // * FP32 outputs: the tensor core's accumulation truncates, so a chain of 448 instructions (K = 7168) is 8e-6 of the result
 //   off. Accumulations of kLnChunk blocks are added in registers with rounding instead: 5e-7, at 57.5 us instead of 53.8
 //   (16384 x 256 x 7168). BF16 outputs, whose rounding is 250 times that, take the chain.
-// What bounds it: large products the operands' way into shared memory, 48 KB a block in 694 clocks against 512 of MMA
-// (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a burst; the tiles' order counts, 771 us with the row tiles of one
-// weight tile one after another). Measured and left out: 256 x 256 tiles, two accumulators that share the weights, three
-// stages of 64 KB (626 us against 577); prefetches into L2 ahead of the ring (router of 16384 tokens 57.8 against 57.4 us,
-// 64 x 4096 x 7168 18.1 against 17.4); CTAs that start at different places of K (no difference); two CTAs an SM with
-// half the ring (64 x 7168 x 2048 11.2 us against 9.1).
+// What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB) and
+// read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
+// burst; 615 to 640 at the power limit. The tiles' order counts: 771 us with the row tiles of one weight tile one after
+// another). Small tiles the same: an MMA reads its 128 token rows whatever it has of them, so 16 to 48 columns take 70 to
+// 90 clocks as 256 take 190. Measured and left out: 256 x 256 tiles, two accumulators that share the weights, with three
+// stages of 64 KB (626 us against 577) and with six of half as many values (809: TMA takes rows of 64 bytes no faster than
+// rows of 128); prefetches into L2 ahead of the ring (router of 16384 tokens 57.8 against 57.4 us, 64 x 4096 x 7168 18.1
+// against 17.4); CTAs that start at different places of K (no difference); two CTAs an SM with half the ring (64 x 7168 x
+// 2048 11.2 us against 9.1); partial sums with a row's columns together (512 x 256 x 7168 17 us against 12.5).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
