@@ -24,8 +24,8 @@
 // What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB) and
 // read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
 // burst; 615 to 640 at the power limit. The tiles' order counts: 771 us with the row tiles of one weight tile one after
-// another). Small tiles the same: an MMA reads its 128 token rows whatever it has of them, so 16 to 48 columns take 70 to
-// 90 clocks as 256 take 190. Measured and left out: 256 x 256 tiles, two accumulators that share the weights, with three
+// another). Small tiles the same: an MMA reads its 128 (up to 64 tokens: 64) token rows whatever it has of them, so one of
+// 48 columns takes 70 clocks as one of 256 takes 190 (64 x 7168 x 2048: 8.1 us with 128 rows, 7.0 with 64). Measured and left out: 256 x 256 tiles, two accumulators that share the weights, with three
 // stages of 64 KB (626 us against 577) and with six of half as many values (809: TMA takes rows of 64 bytes no faster than
 // rows of 128); prefetches into L2 ahead of the ring (router of 16384 tokens 57.8 against 57.4 us, 64 x 4096 x 7168 18.1
 // against 17.4); CTAs that start at different places of K (no difference); two CTAs an SM with half the ring (64 x 7168 x
@@ -431,6 +431,7 @@ struct LnTcArgs {
   int single;  // first stage that is loaded block by block
   int chunk;   // stages that one accumulation in tensor memory takes
   int split;   // units a tile
+  int half_m;  // MMAs of 64 token rows
   int units, stages;
   uint32_t tmem_cols;  // allocated: both buffers
   float* partial;      // [units][tile_n][rows]
@@ -456,9 +457,9 @@ constexpr size_t kLnSmemBytes = kLnRingBytes + 1024 + sizeof(LnShared);
 static_assert(kLnSmemBytes <= 232448, "shared memory per CTA");
 static_assert(sizeof(LnShared) >= 128 * 128, "an MMA of the last stage reads 128 rows");
 
-// Instruction descriptor of tcgen05.mma kind::f16 with BF16 A and B, both K-major, FP32 accumulation, shape 128 x N.
-__device__ __forceinline__ uint32_t ln_idesc(int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (128u >> 4 << 24);
+// Instruction descriptor of tcgen05.mma kind::f16 with BF16 A and B, both K-major, FP32 accumulation, shape M x N.
+__device__ __forceinline__ uint32_t ln_idesc(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // D[tmem] (+)= A[smem] x B[smem]^T, 16 values of K, issued by one thread.
 __device__ __forceinline__ void ln_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     // ------------------------------------------------------------ MMA
     uint32_t s = 0, phase = 0, n = 0;  // n: accumulations begun
     bool ok = true;
-    const uint32_t idesc = ln_idesc(a.tile_n);
+    const uint32_t idesc = ln_idesc(a.half_m ? 64 : 128, a.tile_n);
     const uint64_t desc0 = sw128_desc(smem_u32(ring));
     for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
@@ -621,14 +622,15 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     if (CHUNKED) reg_inc<kLnEpiRegs>();
     // A warp reads the 32 tensor-memory lanes (rows) its number allows; the two warps of a quarter share the columns.
     const int quad = warp & 3, half = warp >> 2;
-    const int row = 32 * quad + lane;
+    // Of 128 rows a warp's lanes hold 32; of 64 rows the first 16 of its lanes hold 16.
+    const int each_quad = a.half_m ? 16 : 32, row = each_quad * quad + lane;
     float* turn = S.turn[warp];
     uint32_t n = 0;
     bool ok = true;
     for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
       const int m0 = a.tile_m * t.m, n0 = a.tile_n * t.n;
-      const int rows = min(a.tile_m, a.e.M - m0) - 32 * quad;  // of this warp's 32
+      const int rows = min(each_quad, min(a.tile_m, a.e.M - m0) - each_quad * quad);  // of this warp
       uint32_t base = 0;  // this thread's row of the accumulator, from the columns of its half
       auto wait = [&]() {
         ok = mbar_wait_spin(&S.tfull[n & 1], (n >> 1) & 1, a.timeout_ns, abort);
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       // This thread's column chunks: 32 i + 16 half.
       auto chunk = [&](int c) {
         LnChunk k;
-        k.row = m0 + 32 * quad;
+        k.row = m0 + each_quad * quad;
         k.rows = rows;
         k.n = n0 + c + 16 * half;
         k.cols = min(16, a.e.N - k.n);
@@ -695,7 +697,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
             float z[16];
             tmem_ld_issue(base + c, z);
             tmem_ld_join(z);
-            if (row < a.rows) {
+            if (lane < rows) {
 #pragma unroll
               for (int k = 0; k < 16; ++k) __stcg(part + (c + k) * a.rows, z[k]);
             }
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-            if (row < a.rows) {
+            if (lane < rows) {
               const float* from = tile + c * a.rows;
 #pragma unroll 4
               for (int s = 0; s < a.split; ++s)
@@ -794,10 +796,11 @@ static bool ln_few(int M, int N, int K) {
   return M <= 8 || (M <= kLnFewMax && static_cast<long long>(N) * K <= (1 << 23));
 }
 
-// How a product in tiles is cut: by what the ways cost, in clocks, to within 2 % of the best way of 25 shapes that were
-// swept (tokens 16 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block takes its bytes at 78 a clock (tokens and weights
-// arrive through one port), 385 clocks at least; a tile's epilogue 4000 for 256 columns, hidden behind the next tile's
-// products but for the last one's; cutting K 10,500 and the partial sums' way through L2.
+// How a product in tiles is cut: by what the ways cost, in clocks, to within 1.3 % on average of the best way of 34 shapes
+// that were swept with their operands out of L2 (tokens 17 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block costs
+// shared memory's time at 128 bytes a clock: what is written, the box's token rows and the weight rows, and what an MMA
+// reads, 128 (or 64) token rows and the weight rows again, each of them 128 bytes. Cutting K costs 8000 clocks and the partial
+// sums' way at 20 bytes a clock.
 struct LnPlan {
   int tile_m, tile_n, tiles_m, tiles_n, blocks, split;
 };
@@ -812,12 +815,10 @@ static LnPlan ln_plan(int M, int N, int K, int sms) {
   for (int tile_n = 16; tile_n <= 256 && tile_n < N + 16; tile_n += 16) {
     const int tiles_n = (N + tile_n - 1) / tile_n;
     const long long tiles = static_cast<long long>(p.tiles_m) * tiles_n;
-    const long long bytes = (box_m + tile_n) * 128ll, part = static_cast<long long>(p.tile_m) * tile_n * 4;
-    const long long block = bytes / 78 > 385 ? bytes / 78 : 385, finish = 4000ll * tile_n / 256;
+    const long long block = box_m + (p.tile_m <= 64 ? 64 : 128) + 2 * tile_n;
     for (int split = 1; split <= 16 && split <= p.blocks && (split == 1 || tiles * split <= sms); ++split) {
-      const long long waves = (tiles * split + sms - 1) / sms, main = (p.blocks + split - 1) / split * block;
-      long long cost = waves * (main > finish ? main : finish) + finish;
-      if (split > 1) cost += 10500 + part / 122 + split * part / 11;
+      long long cost = (tiles * split + sms - 1) / sms * ((p.blocks + split - 1) / split) * block;
+      if (split > 1) cost += 8000 + split * (4ll * p.tile_m * tile_n) / 20;
       if (best < 0 || cost < best) {
         best = cost;
         p.tile_n = tile_n;
@@ -923,6 +924,7 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   a.e = ln_epilogue(l);
   a.rows = p.tile_m;
   a.tile_m = p.tile_m;
+  a.half_m = p.tile_m <= 64;
   a.box_m = (p.tile_m + 7) / 8 * 8;
   a.tiles_m = p.tiles_m;
   a.tiles_n = p.tiles_n;
