@@ -16,7 +16,9 @@
 // What bounds it: 16384 tokens of 256 experts, 24 us: of a CTA's 43,000 clocks the picks take 27,100 (three or four
 // tokens a warp, one after another), the sums over all CTAs' counts 6,600, the meeting 4,300, the places 3,000; issue slots
 // are half used, and the largest stall is the CTA barrier. 1533 tokens of 896 experts, 23 us (96 CTAs, 39,800 clocks):
-// picks 19,100, sums 8,500, meeting 8,300. One token 6 us: latency.
+// picks 19,100, sums 8,500, meeting 8,300. One token 6 us: latency. Four of eight groups: 16384 x 256 6 us more, the groups' sums by
+// a tree over the lanes that hold them (16 us more with a loop over the groups, which groups that share a lane take:
+// 1533 x 896 in eight 40 us).
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
@@ -274,19 +276,30 @@ __device__ __forceinline__ void rt_pick_scored(const RtArgs& a, const float (&bi
     ky[j] = J * lane + j < a.E ? max(1u, ordered_key(a.bias != nullptr ? p[j] : l[j])) : 0u;
   }
   if (a.top_groups < a.groups) {
-    uint32_t gk[J];
+    uint32_t open;
+    if (a.bias != nullptr || a.group_top == 1) {
+      open = rt_groups<J>(a, ky, lane);
+    } else {
+      uint32_t gk[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      gk[j] = a.bias != nullptr || a.group_top == 1 || ky[j] == 0u ? ky[j] : max(1u, ordered_key(p[j]));
-    const uint32_t open = rt_groups<J>(a, gk, lane);
-    int g = J * lane / a.group_size, next = (g + 1) * a.group_size;
+      for (int j = 0; j < J; ++j) gk[j] = ky[j] == 0u ? 0u : max(1u, ordered_key(p[j]));
+      open = rt_groups<J>(a, gk, lane);
+    }
+    int g = J * lane / a.group_size;
+    if (a.group_size % J == 0) {  // one group a lane (past the last expert: keys are 0 already)
+      const bool out = !(open >> (g & 31) & 1u);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (J * lane + j == next) {
-        ++g;
-        next += a.group_size;
+      for (int j = 0; j < J; ++j) ky[j] = out ? 0u : ky[j];
+    } else {
+      int next = (g + 1) * a.group_size;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (J * lane + j == next) {
+          ++g;
+          next += a.group_size;
+        }
+        if (g < 32 && !(open >> g & 1u)) ky[j] = 0u;
       }
-      if (g < 32 && !(open >> g & 1u)) ky[j] = 0u;
     }
   }
   uint32_t best = 0u;
