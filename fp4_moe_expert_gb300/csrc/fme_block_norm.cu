@@ -12,10 +12,10 @@
 // fme_add_rmsnorm_fp8's.
 //
 // HBM-bound: 2 bytes a value for each row read, 4 to 5 written; what stands in the way are instructions, so values are worked
-// on in pairs (f32x2) and divisions are taken by one residual step (16384 x 7168 with a gate for every value 270 -> 213
-// us with the copies ahead and both, 6.1 TB/s; 4096 tokens of 8 routes 137 -> 110 us, 6.7 TB/s, the copy rate). Measured
-// and left out: four chunks a thread (16384 x 7168 with a gate 229 us), one (284), five rows ahead (217), a CTA a
-// row without copies ahead (269).
+// on in pairs (f32x2), divisions are taken by one residual step, and rows that fill every thread's chunks have a kernel of their
+// own (16384 x 7168 with a gate for every value 270 -> 201 us with the copies ahead and all three, 6.4 TB/s; 4096 tokens of 8
+// routes 137 -> 109 us, 6.7 TB/s, the copy rate). Measured and left out (against 213 us of the gated form before the last
+// step): four chunks a thread 229, one 284, five rows ahead 217, a CTA a row without copies ahead 269.
 #include "fme_common.cuh"
 #include "fme_internal.h"
 
@@ -36,6 +36,7 @@ struct BnArgs {
   const __nv_bfloat16* gamma;
   long long ldx, ldg, ldr;
   int top_k, T, H;
+  long long jump_x, step_shared, step_gate, step_residual;  // from a CTA's token's rows to its next one's, in 16 bytes
   float residual_scale, eps, inv_h;
   int quant, ue8m0;
   uint8_t* q;
@@ -116,7 +117,7 @@ __device__ __forceinline__ float bn_recip(float s) {
 }
 
 // Walks the rows that tokens' sums need, in the order of their use: of a token the block's (top_k of them or one), the
-// shared expert's, the gate, the residual; then those of the token `stride` on.
+// shared expert's, the gate, the residual.
 struct BnWalk {
   const uint4 *x, *shared, *gate, *residual;  // of the token, at this thread's first chunk
   int i;                                      // the next row
@@ -158,7 +159,7 @@ __device__ __forceinline__ void bn_token(const BnArgs& a, int t, int first, int 
       for (int k = 0; k < 4; ++k) v[c][k] = 0ull;
     const float* weights = a.route_weights + static_cast<size_t>(t) * a.top_k;
     for (int r = 0; r < a.top_k; ++r) {
-      const float w = t < a.T ? __ldg(weights + r) : 0.0f;
+      const float w = __ldg(weights + r);
       load([&](int c, const uint4& p) {
         BnPair o[4];
         bn_unpack(p, o);
@@ -271,15 +272,16 @@ __device__ __forceinline__ void bn_token(const BnArgs& a, int t, int first, int 
 }
 
 // Narrow rows: a warp a row.
-template <int CH>
+template <int CH, bool WHOLE>
 __global__ void __launch_bounds__(32 * kBnSmallRows) block_norm_small_kernel(const BnArgs a) {
   __shared__ float part[2][32];
   const int lane = threadIdx.x & 31, t = blockIdx.x * kBnSmallRows + (threadIdx.x >> 5);
   griddep_launch_dependents();  // the next kernel's start may overlap this one's end; it waits before it reads
   griddep_wait();
+  if (t >= a.T) return;
   bool mine[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) mine[c] = t < a.T && lane + 32 * c < a.H / 8;
+  for (int c = 0; c < CH; ++c) mine[c] = WHOLE || lane + 32 * c < a.H / 8;
   BnWalk walk = bn_walk(a, t, lane);
   bn_token<CH, true>(a, t, lane, 32, mine, part, [&](auto use) {
     const uint4* from = bn_next(a, walk);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(32 * kBnSmallRows) block_norm_small_kernel(con
 // Wide rows: persistent CTAs, a token at a time. A thread's chunks are the same columns in every row, so it copies them itself,
 // kBnAhead rows ahead (of this token or the next), into places of shared memory that are its own, and no barrier stands
 // between a copy and its use.
-template <int MOST>
+template <int MOST, bool WHOLE>
 __global__ void __launch_bounds__(MOST, kBnThreads / MOST) block_norm_kernel(const BnArgs a, const int rows) {
   constexpr int CH = kBnChunks, S = kBnAhead + 1;
   extern __shared__ uint4 ring[];  // [S][CH][threads]
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(MOST, kBnThreads / MOST) block_norm_kernel(con
   griddep_wait();
   bool mine[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) mine[c] = tid + threads * c < a.H / 8;
+  for (int c = 0; c < CH; ++c) mine[c] = WHOLE || tid + threads * c < a.H / 8;
   uint4* const begin = ring + tid;
   uint4* const end = begin + S * CH * threads;
   int at = blockIdx.x;  // the token of the next row to ask for
@@ -322,7 +324,11 @@ __global__ void __launch_bounds__(MOST, kBnThreads / MOST) block_norm_kernel(con
     if (into == end) into = begin;
     if (walk.i == rows) {
       at += gridDim.x;
-      walk = bn_walk(a, at, tid);
+      walk.x += a.jump_x;
+      walk.shared += a.step_shared;
+      walk.gate += a.step_gate;
+      walk.residual += a.step_residual;
+      walk.i = 0;
     }
   };
 #pragma unroll 1
@@ -341,15 +347,20 @@ __global__ void __launch_bounds__(MOST, kBnThreads / MOST) block_norm_kernel(con
     });
 }
 
-template <int MOST>
-static cudaError_t bn_launch(const BnArgs& a, int rows, int sms, int dev, cudaStream_t st) {
+template <int MOST, bool WHOLE>
+static cudaError_t bn_launch(BnArgs a, int rows, int sms, int dev, cudaStream_t st) {
   const int threads = (a.H / 8 + 32 * kBnChunks - 1) / (32 * kBnChunks) * 32;
   const size_t place = (kBnAhead + 1) * kBnChunks * sizeof(uint4), smem = place * threads;  // place: a thread's
-  const void* kernel = reinterpret_cast<const void*>(block_norm_kernel<MOST>);
+  const void* kernel = reinterpret_cast<const void*>(block_norm_kernel<MOST, WHOLE>);
   if (!ensure_smem_attr(dev, kernel, place * MOST)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
   const int most = sms * (kBnThreads / threads);  // as many as an SM's registers hold
-  cfg.gridDim = dim3(static_cast<unsigned>(a.T < most ? a.T : most));
+  const long long grid = a.T < most ? a.T : most, n = a.top_k == 0 ? 1 : a.top_k;
+  a.jump_x = (grid - 1) * n * (a.ldx / 8);
+  a.step_shared = grid * (a.H / 8);
+  a.step_gate = grid * (a.ldg / 8);
+  a.step_residual = grid * (a.ldr / 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -358,10 +369,10 @@ static cudaError_t bn_launch(const BnArgs& a, int rows, int sms, int dev, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_norm_kernel<MOST>, a, rows);
+  return cudaLaunchKernelEx(&cfg, block_norm_kernel<MOST, WHOLE>, a, rows);
 }
 
-template <int CH>
+template <int CH, bool WHOLE>
 static cudaError_t bn_launch_small(const BnArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.T + kBnSmallRows - 1) / kBnSmallRows));
@@ -372,7 +383,7 @@ static cudaError_t bn_launch_small(const BnArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_norm_small_kernel<CH>, a);
+  return cudaLaunchKernelEx(&cfg, block_norm_small_kernel<CH, WHOLE>, a);
 }
 
 int block_norm(const BlockNorm& b, cudaStream_t st) {
@@ -405,12 +416,21 @@ int block_norm(const BlockNorm& b, cudaStream_t st) {
   if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
   const int chunks = a.H / 8;
   const int rows = (a.top_k == 0 ? 1 : a.top_k) + (a.shared_out != nullptr) + (a.gate != nullptr) + (a.residual != nullptr);
-  // A warp a row up to 1024 values (16384 tokens of 1024: 26.2 us, of the wide kernel 29.3).
-  const cudaError_t err = chunks <= 32     ? bn_launch_small<1>(a, st)
-                          : chunks <= 64   ? bn_launch_small<2>(a, st)
-                          : chunks <= 128  ? bn_launch_small<4>(a, st)
-                          : chunks <= 1024 ? bn_launch<512>(a, rows, sms, dev, st)
-                                           : bn_launch<1024>(a, rows, sms, dev, st);
+  // A warp a row up to 1024 values (16384 tokens of 1024: 26 us, of the wide kernel 29). Rows that fill every thread's chunks
+  // have no values to ask about (16384 x 7168 with a gate 213 -> 201 us).
+  cudaError_t err;
+  if (chunks <= 32)
+    err = chunks == 32 ? bn_launch_small<1, true>(a, st) : bn_launch_small<1, false>(a, st);
+  else if (chunks <= 64)
+    err = chunks == 64 ? bn_launch_small<2, true>(a, st) : bn_launch_small<2, false>(a, st);
+  else if (chunks <= 128)
+    err = chunks == 128 ? bn_launch_small<4, true>(a, st) : bn_launch_small<4, false>(a, st);
+  else if (chunks <= 1024)
+    err = chunks % (32 * kBnChunks) == 0 ? bn_launch<512, true>(a, rows, sms, dev, st)
+                                         : bn_launch<512, false>(a, rows, sms, dev, st);
+  else
+    err = chunks % (32 * kBnChunks) == 0 ? bn_launch<1024, true>(a, rows, sms, dev, st)
+                                         : bn_launch<1024, false>(a, rows, sms, dev, st);
   if (err != cudaSuccess) return set_last_error(FME_ECUDA, "block norm launch: %s", cudaGetErrorString(err));
   return FME_OK;
 }
