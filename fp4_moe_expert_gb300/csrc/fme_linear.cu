@@ -433,11 +433,11 @@ struct LnTcArgs {
   int split;   // units a tile
   int half_m;  // MMAs of 64 token rows
   int units, stages;
-  uint32_t tmem_cols;  // allocated: both buffers
-  float* partial;      // [units][tile_n][rows]
-  int rows;            // rows of a partial tile
+  uint32_t tmem_cols;  // allocated: both buffers, or the only one
+  float4* partial;     // [units][rows / 32][tile_n / 4][32] of four columns
+  int rows;            // rows of a partial tile: 32 a quarter
   uint32_t* err;
-  uint32_t* arrived;  // [tiles], zero between calls
+  uint32_t* arrived;  // [tiles][warps], zero between calls
   unsigned long long timeout_ns;
   LnEpilogue e;
 };
@@ -450,7 +450,6 @@ struct LnShared {
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  int last;
   float turn[kLnEpiWarps][32 * 17];
 };
 constexpr size_t kLnSmemBytes = kLnRingBytes + 1024 + sizeof(LnShared);
@@ -468,6 +467,13 @@ __device__ __forceinline__ void ln_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Counts an arrival: what this warp wrote before stands for whoever counts after.
+__device__ __forceinline__ uint32_t ln_arrive(uint32_t* counter) {
+  uint32_t before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  return before;
 }
 
 struct LnUnit {
@@ -528,6 +534,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
   const uint32_t tmem = S.tmem;
   const volatile int* abort = &S.abort;
   const int first = blockIdx.x, step = gridDim.x;
+  constexpr int JOIN = CHUNKED ? 2 : 4;  // partial sums on their way at once, as the registers allow
 
   if (CHUNKED && warp >= kLnEpiWarps) reg_dec<kLnOtherRegs>();
 
@@ -578,17 +585,23 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA
-    uint32_t s = 0, phase = 0, n = 0;  // n: accumulations begun
+    uint32_t s = 0, phase = 0, n = 0, b = 0, d = 0;  // n: buffers begun, b and d: the current one and its accumulator
     bool ok = true;
     const uint32_t idesc = ln_idesc(a.half_m ? 64 : 128, a.tile_n);
     const uint64_t desc0 = sw128_desc(smem_u32(ring));
     for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
-      for (int c0 = t.g0; c0 < t.g1 && ok; c0 += a.chunk, ++n) {
+      for (int c0 = t.g0; c0 < t.g1 && ok; c0 += a.chunk) {
         const int c1 = min(t.g1, c0 + a.chunk);
-        const uint32_t b = n & 1, d = tmem + b * (a.tmem_cols / 2);
-        ok = mbar_wait_spin(&S.tempty[b], ((n >> 1) & 1) ^ 1, a.timeout_ns, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (CHUNKED || c0 == t.g0) {
+          b = n & 1;
+          d = tmem + b * (a.tmem_cols / 2);
+          ok = mbar_wait_spin(&S.tempty[b], ((n >> 1) & 1) ^ 1, a.timeout_ns, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          ++n;
+        } else {
+          d += a.tile_n;
+        }
         for (int g = c0; g < c1 && ok; ++g) {
           ok = mbar_wait_spin(&S.full[s], phase, a.timeout_ns, abort);
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
 #pragma unroll
               for (int i = 0; i < 4; ++i) ln_mma(d, ad + 2 * i, bd + 2 * i, idesc, g > c0 || j + i != 0);
             tc_commit(&S.done[s]);
-            if (g == c1 - 1) tc_commit(&S.tfull[b]);
+            if (g == (CHUNKED ? c1 : t.g1) - 1) tc_commit(&S.tfull[b]);
           }
           __syncwarp();
           if (++s == static_cast<uint32_t>(a.stages)) s = 0, phase ^= 1;
@@ -623,7 +636,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     // A warp reads the 32 tensor-memory lanes (rows) its number allows; the two warps of a quarter share the columns.
     const int quad = warp & 3, half = warp >> 2;
     // Of 128 rows a warp's lanes hold 32; of 64 rows the first 16 of its lanes hold 16.
-    const int each_quad = a.half_m ? 16 : 32, row = each_quad * quad + lane;
+    const int each_quad = a.half_m ? 16 : 32;
     float* turn = S.turn[warp];
     uint32_t n = 0;
     bool ok = true;
@@ -684,57 +697,78 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       } else {
         wait();
       }
-      // Uniform over the eight warps where a barrier follows, so that none is left waiting there.
-      if (a.split > 1) ok = !named_bar_or(1, 32 * kLnEpiWarps, !ok);
-      if (!ok) break;
-      bool mine = true;  // this unit finishes the tile
-      const size_t each = static_cast<size_t>(a.tile_n) * a.rows;
-      float* tile = a.partial + static_cast<size_t>(t.tile) * a.split * each + 16 * half * a.rows + row;
-      if (a.split > 1) {
-        float* part = tile + (u - t.tile * a.split) * each;
-        if (rows > 0)
-          for (int c = 0; c + 16 * half < a.tile_n; c += 32) {
-            float z[16];
-            tmem_ld_issue(base + c, z);
-            tmem_ld_join(z);
-            if (lane < rows) {
+      // 16 columns of the unit's sums: of one accumulator, or of all that it has.
+      auto sums = [&](int c, float (&z)[16]) {
+        tmem_ld_issue(base + c, z);
+        tmem_ld_join(z);
+        if (!CHUNKED)
+#pragma unroll 1
+          for (int c0 = t.g0 + a.chunk, at = base + c; c0 < t.g1; c0 += a.chunk) {
+            float d[16];
+            tmem_ld_issue(at += a.tile_n, d);
+            tmem_ld_join(d);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) __stcg(part + (c + k) * a.rows, z[k]);
-            }
+            for (int k = 0; k < 16; ++k) z[k] = __fadd_rn(z[k], d[k]);
           }
-        __threadfence();
-        named_bar_sync(1, 32 * kLnEpiWarps);
-        if (tid == 0) {
-          __threadfence();
-          const uint32_t before = atomicAdd(a.arrived + t.tile, 1u);
-          S.last = before == static_cast<uint32_t>(a.split) - 1u;
-          if (S.last) a.arrived[t.tile] = 0u;
+      };
+      if (!ok) break;
+      bool mine = rows > 0;  // this warp finishes its part of the tile
+      // Partial sums: of a unit a part for each quarter of the rows, of that 16 columns at a time, of those four at a time,
+      // of those a row a lane.
+      const size_t each = static_cast<size_t>(a.tile_n) * a.rows;
+      float4* tile = a.partial + (static_cast<size_t>(t.tile) * a.split * each + (a.tile_n * quad + 16 * half) * 32) / 4 + lane;
+      if (mine && a.split > 1) {
+        float4* part = tile + (u - t.tile * a.split) * (each / 4);
+        for (int c = 0; has(c); c += 32) {
+          float z[16];
+          sums(c, z);
+          if (lane < rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              __stcg(part + (c / 4 + k) * 32, make_float4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]));
+          }
+        }
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) {
+          uint32_t* arrived = a.arrived + t.tile * kLnEpiWarps + warp;
+          before = ln_arrive(arrived);
+          if (before == static_cast<uint32_t>(a.split) - 1u) *arrived = 0u;
           // A count that no call left: the tile may have no last unit, or one too early.
           if (before >= static_cast<uint32_t>(a.split)) atomicOr(a.err, kErrCrossWait);
-          __threadfence();
         }
-        named_bar_sync(1, 32 * kLnEpiWarps);
-        mine = S.last;
-        __threadfence();
+        mine = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(a.split) - 1u;
       }
-      if (mine && rows > 0) {
+      if (mine) {
         for (int c = 0; has(c); c += 32) {
           const LnChunk k = chunk(c);
           uint32_t raw[16];
           ln_residual(a.e, k, lane, raw);
           float z[16];
           if (a.split == 1) {
-            tmem_ld_issue(base + c, z);
-            tmem_ld_join(z);
+            sums(c, z);
           } else {
+            // In K's order, four units' partial sums on their way at once; lanes past the rows read the last row's.
+            const float4* from = tile + (c / 4) * 32 - max(lane - (rows - 1), 0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-            if (lane < rows) {
-              const float* from = tile + c * a.rows;
-#pragma unroll 4
-              for (int s = 0; s < a.split; ++s)
+#pragma unroll 1
+            for (int s = 0; s < a.split; s += JOIN, from += JOIN * (each / 4)) {
+              float4 p[JOIN][4];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], __ldcg(from + s * each + i * a.rows));
+              for (int b = 0; b < JOIN; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  p[b][i] = s + b < a.split ? __ldcg(from + b * (each / 4) + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int b = 0; b < JOIN; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  z[4 * i] = __fadd_rn(z[4 * i], p[b][i].x);
+                  z[4 * i + 1] = __fadd_rn(z[4 * i + 1], p[b][i].y);
+                  z[4 * i + 2] = __fadd_rn(z[4 * i + 2], p[b][i].z);
+                  z[4 * i + 3] = __fadd_rn(z[4 * i + 3], p[b][i].w);
+                }
             }
           }
           ln_finish16(a.e, z, k.n);
@@ -830,6 +864,12 @@ static LnPlan ln_plan(int M, int N, int K, int sms) {
   return p;
 }
 
+// Rows of a partial tile: 32 for each of its quarters of 32 (or 16).
+static int ln_partial_rows(const LnPlan& p) {
+  const int quarter = p.tile_m <= 64 ? 16 : 32;
+  return (p.tile_m + quarter - 1) / quarter * 32;
+}
+
 static int ln_sms(int dev) {
   const int sms = device_sm_count(dev);
   return sms < kLnMaxUnits ? sms : kLnMaxUnits;
@@ -843,7 +883,7 @@ size_t linear_workspace_bytes(int M, int N, int K) {
   const LnPlan p = ln_plan(M, N, K, sms > 0 ? sms : 152);
   if (p.split == 1) return kLnHeader;
   const size_t need =
-      kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * p.tile_m * sizeof(float);
+      kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * ln_partial_rows(p) * sizeof(float);
   size_t bytes = 65536;
   while (bytes < need) bytes *= 2;
   return bytes;
@@ -922,7 +962,7 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   const LnPlan p = ln_plan(l.M, l.N, l.K, sms);
   LnTcArgs a = {};
   a.e = ln_epilogue(l);
-  a.rows = p.tile_m;
+  a.rows = ln_partial_rows(p);
   a.tile_m = p.tile_m;
   a.half_m = p.tile_m <= 64;
   a.box_m = (p.tile_m + 7) / 8 * 8;
@@ -943,8 +983,13 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   a.units = p.tiles_m * p.tiles_n * a.split;
   a.stages = kLnRingBytes / (a.slices * block);
   if (a.stages > kLnMaxStages) a.stages = kLnMaxStages;
+  // A unit's accumulations stay side by side in tensor memory where they fit (two buffers of them for CTAs of several units), and
+  // meet in registers as they end where not.
+  const int most = (a.groups + a.split - 1) / a.split, each = (most + a.chunk - 1) / a.chunk * a.tile_n;
+  const int beside = a.units <= sms ? each : 2 * each;
+  const bool chunked = beside > 512;
   a.tmem_cols = 32;
-  while (a.tmem_cols < 2u * a.tile_n) a.tmem_cols *= 2;
+  while (a.tmem_cols < static_cast<uint32_t>(chunked ? 2 * a.tile_n : beside)) a.tmem_cols *= 2;
   if (!ln_map(&a.mapx1, l.x, l.M, l.K, l.ldx, a.box_m, 0) || !ln_map(&a.mapw1, l.w, l.N, l.K, l.ldw, a.tile_n, 0) ||
       (l.K >= kLnKBlock && (!ln_map(&a.mapx, l.x, l.M, l.K, l.ldx, a.box_m, a.slices) ||
                             !ln_map(&a.mapw, l.w, l.N, l.K, l.ldw, a.tile_n, a.slices))))
@@ -955,9 +1000,9 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   }
   a.err = static_cast<uint32_t*>(workspace);
   a.arrived = a.err + 64;
-  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kLnHeader);
+  a.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + kLnHeader);
   a.timeout_ns = wait_timeout_ns();
-  const void* kernel = reinterpret_cast<const void*>(a.chunk < a.groups ? linear_tc_kernel<true> : linear_tc_kernel<false>);
+  const void* kernel = reinterpret_cast<const void*>(chunked ? linear_tc_kernel<true> : linear_tc_kernel<false>);
   if (!ensure_smem_attr(dev, kernel, kLnSmemBytes)) return FME_ECUDA;
   return ln_launch(kernel, a.units < sms ? a.units : sms, kLnThreads,
                    kLnSmemBytes, &a, st);
