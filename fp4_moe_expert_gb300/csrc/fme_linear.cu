@@ -823,18 +823,18 @@ static bool ln_map(CUtensorMap* map, const void* base, int rows, int cols, long 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether a product goes to the kernels of few tokens. Measured with the weights out of L2, they against tiles: 8 tokens of
-// 256 x 7168 4.6 us / 11.1, of 7168 x 2048 8.2 / 10.3, of 4096 x 7168 12.6 / 30; 16 tokens of 256 x 7168 5.7 / 10.1, of
-// 1500 x 2664 6.6 / 9.3, of 7168 x 2048 14.3 / 10.3, of 4096 x 7168 22.8 / 21.9.
+// Whether a product goes to the kernels of few tokens. Measured with the weights out of L2, they against tiles (us): 8 tokens of
+// 256 x 7168 4.6 / 6.3, of 7168 x 2048 8.4 / 8.9, of 4096 x 7168 13.1 / 14.6; 16 tokens of 256 x 7168 5.8 / 6.4, of 1024 x
+// 4096 4.9 / 5.8, of 7168 x 1024 9.3 / 6.6, of 4096 x 7168 23 / 14.5.
 static bool ln_few(int M, int N, int K) {
-  return M <= 8 || (M <= kLnFewMax && static_cast<long long>(N) * K <= (1 << 23));
+  return M <= 8 || (M <= kLnFewMax && static_cast<long long>(N) * K <= (1 << 22));
 }
 
-// How a product in tiles is cut: by what the ways cost, in clocks, to within 1.3 % on average of the best way of 34 shapes
-// that were swept with their operands out of L2 (tokens 17 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block costs
-// shared memory's time at 128 bytes a clock: what is written, the box's token rows and the weight rows, and what an MMA
-// reads, 128 (or 64) token rows and the weight rows again, each of them 128 bytes. Cutting K costs 8000 clocks and the partial
-// sums' way at 20 bytes a clock.
+// How a product in tiles is cut: by what the ways cost, in clocks, to within 1 % on average of the best way of 42 shapes that
+// were swept with their operands out of L2 (tokens 17 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block costs shared
+// memory's time at 128 bytes a clock: what is written, the box's token rows and the weight rows, and what an MMA reads, 128 (or
+// 64) token rows and the weight rows again, each of them 128 bytes; all blocks together at least HBM's, 3500 bytes a clock.
+// Cutting K costs 2500 clocks and the partial sums' way at 20 bytes a clock.
 struct LnPlan {
   int tile_m, tile_n, tiles_m, tiles_n, blocks, split;
 };
@@ -845,6 +845,7 @@ static LnPlan ln_plan(int M, int N, int K, int sms) {
   p.tile_m = p.tiles_m == 1 ? M : ((M + p.tiles_m - 1) / p.tiles_m + 7) / 8 * 8;
   p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
   const int box_m = (p.tile_m + 7) / 8 * 8;
+  const long long hbm = 2ll * K * (static_cast<long long>(M) + N) / 3500;
   long long best = -1;
   for (int tile_n = 16; tile_n <= 256 && tile_n < N + 16; tile_n += 16) {
     const int tiles_n = (N + tile_n - 1) / tile_n;
@@ -852,7 +853,8 @@ static LnPlan ln_plan(int M, int N, int K, int sms) {
     const long long block = box_m + (p.tile_m <= 64 ? 64 : 128) + 2 * tile_n;
     for (int split = 1; split <= 16 && split <= p.blocks && (split == 1 || tiles * split <= sms); ++split) {
       long long cost = (tiles * split + sms - 1) / sms * ((p.blocks + split - 1) / split) * block;
-      if (split > 1) cost += 8000 + split * (4ll * p.tile_m * tile_n) / 20;
+      if (cost < hbm) cost = hbm;
+      if (split > 1) cost += 2500 + split * (4ll * p.tile_m * tile_n) / 20;
       if (best < 0 || cost < best) {
         best = cost;
         p.tile_n = tile_n;
