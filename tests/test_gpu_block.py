@@ -240,6 +240,40 @@ def test_route_groups_equals_route_without_groups(fme):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("T,E,k,groups,top_groups,group_top", [
+    (40, 896, 16, 8, 1, 2), (40, 896, 32, 8, 2, 1), (25, 500, 20, 10, 1, 2), (33, 1000, 32, 8, 1, 2), (31, 130, 8, 13, 4, 2),
+    (20, 1022, 5, 14, 6, 2), (18, 257, 9, 1, 1, 1), (50, 258, 31, 6, 5, 2), (2000, 999, 7, 27, 9, 2)])
+def test_route_groups_in_few_lanes_or_across_two(fme, T, E, k, groups, top_groups, group_top):
+    for i, (score, bias, bf16) in enumerate((("softmax", 0.1, False), ("sigmoid", 0.3, True))):
+        _check_route(fme, T, E, k, bf16, i, bias, score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+def test_route_groups_more_equal_keys_than_lanes(fme):
+    for E, k in ((896, 16), (256, 8), (1000, 32), (64, 32)):
+        top = list(range(5, E, max(1, E // 45)))[:40]
+        logits = torch.zeros(3, E, device=DEV)
+        logits[1, top] = 1.0
+        logits[2, top[:3]] = 1.0
+        rest = [e for e in range(E) if e not in top[:3]]
+        for ids in (fme.moe_route_groups(logits, None, k)[0], fme.moe_route(logits, torch.zeros(E, device=DEV), k)[0]):
+            assert ids[0].tolist() == list(range(k))
+            assert ids[1].tolist() == top[:k]
+            assert ids[2].tolist() == (top[:3] + rest)[:k]
+
+
+def test_route_of_more_tokens_than_16_bits_count(fme):
+    T, E = 66000, 24
+    logits = torch.zeros(T, E, device=DEV)
+    logits[:, 3] = 2.0
+    second = torch.arange(T, device=DEV) * 7 % 20 + 4
+    logits[torch.arange(T, device=DEV), second] = 1.0
+    ids, _, off, rows, tok = (_np(t) for t in fme.moe_route(logits, torch.zeros(E, device=DEV), 2))
+    assert np.all(ids[:, 0] == 3) and np.array_equal(ids[:, 1], _np(second))
+    assert off[4] - off[3] == T
+    for got, ref in zip((off, rows, tok), prompt.group_routes(ids, E)):
+        assert np.array_equal(got, ref)
+
+
 def test_route_groups_ties(fme):
     T, E, k = 70, 48, 5
     logits = torch.zeros(T, E, device=DEV)
