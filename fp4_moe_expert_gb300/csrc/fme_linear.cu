@@ -8,19 +8,21 @@
 //
 // linear_few_kernel, up to 16 tokens (ln_few): warps hold 16 tokens x 8 weight rows in mma.sync fragments, loaded straight
 // from global memory. A tcgen05 tile needs its operands in shared memory, tensor memory allocated and a pipeline filled,
-// which is 5 us before the first result; here 8 tokens of 256 x 7168 take 4.6 us instead of 11.1.
+// which is 3 us before the first result; here 8 tokens of 256 x 7168 take 4.6 us instead of 6.3.
 //
 // linear_tc_kernel, the rest: one persistent CTA per SM walks units, tiles of up to 128 tokens x tile_n weight rows (a
 // multiple of 16 up to 256) times a share of K. Twelve warps: two load by TMA (tokens and weights, 128-byte swizzle), one
 // issues tcgen05.mma kind::f16, eight read the accumulators (two buffers in tensor memory, so that a tile's epilogue runs
-// beside the next tile's products). Where the tiles are fewer than SMs, K is cut, too: a unit then stores its FP32 sums to
-// the workspace and the last of a tile's units to arrive adds them in K order, whichever it is, so the result does not hang
-// on the order of arrival, and no unit waits for another.
+// beside the next tile's products). Where the tiles are fewer than SMs, K is cut, too: a unit's epilogue warps then store their
+// FP32 sums to the workspace, and of a tile's units the last to have a warp's part there adds them in K order, whichever it is,
+// so the result does not hang on the order of arrival, and no unit waits for another. (A warp's parts in 16-byte pieces, counted
+// by one release and acquire a warp: 128 x 256 x 7168 FP32 9.2 us; value by value behind barriers and fences of the CTA 11.8.)
 // * A stage holds as many K blocks of 64 values as fit 64 KB: a TMA instruction costs its warp about 100 ns whatever it
 //   brings (16 tokens x 7168 x 2048: 12.3 us with one block a stage and one loading warp, 7.8 with eight and two).
 // * FP32 outputs: the tensor core's accumulation truncates, so a chain of 448 instructions (K = 7168) is 8e-6 of the result
-//   off. Accumulations of kLnChunk blocks are added in registers with rounding instead: 5e-7, at 57.5 us instead of 53.8
-//   (16384 x 256 x 7168). BF16 outputs, whose rounding is 250 times that, take the chain.
+//   off. Accumulations of about kLnChunk blocks are added with rounding instead: 5e-7. They stand side by side in tensor memory
+//   where a unit's fit (128 x 256 x 7168 9.2 -> 7.8 us), else they are added in registers as they end (CHUNKED: 16384 x 256 x
+//   7168 57.5 us, the chain 53.8). BF16 outputs, whose rounding is 250 times that, take the chain.
 // What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB) and
 // read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
 // burst; 615 to 640 at the power limit. The tiles' order counts: 771 us with the row tiles of one weight tile one after
@@ -419,7 +421,8 @@ constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows
 constexpr int kLnStageBytes = 65536;
 constexpr int kLnChunk = 8;
 constexpr int kLnGroup = 8;                // weight tiles that are walked together
-constexpr int kLnHeader = 4096;            // workspace: error word, then from byte 256 the tiles' arrival counters
+constexpr int kLnHeader = 4096;            // workspace: error word, then from byte 256 the arrival counters of cut tiles
+static_assert(256 + kLnMaxUnits / 2 * kLnEpiWarps * 4 <= kLnHeader, "a tile that is cut has two units at least");
 
 struct LnTcArgs {
   CUtensorMap mapx, mapx1;  // x [M, K], box box_m rows x 64 values, `slices` (1) K blocks of them
