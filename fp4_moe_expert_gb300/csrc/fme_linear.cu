@@ -869,6 +869,27 @@ static LnPlan ln_plan(int M, int N, int K, int sms) {
   return p;
 }
 
+// The plan of these sizes; the last ones' are kept, since a search is up to 256 ways (64 x 7168 x 2048
+// in a stream 15.8 us, searched twice a call and with four tensor maps; 12.9 with one search kept and two maps).
+static LnPlan ln_plan_kept(int M, int N, int K, int sms) {
+  struct Kept {
+    int M = -1, N, K, sms;
+    LnPlan plan;
+  };
+  constexpr unsigned kKept = 64;
+  thread_local Kept kept[kKept];
+  const unsigned h = (static_cast<unsigned>(M) * 31u + static_cast<unsigned>(N)) * 31u + static_cast<unsigned>(K);
+  Kept& k = kept[(h ^ (h >> 8)) % kKept];
+  if (k.M != M || k.N != N || k.K != K || k.sms != sms) {
+    k.plan = ln_plan(M, N, K, sms);
+    k.M = M;
+    k.N = N;
+    k.K = K;
+    k.sms = sms;
+  }
+  return k.plan;
+}
+
 // Rows of a partial tile: 32 for each of its quarters of 32 (or 16).
 static int ln_partial_rows(const LnPlan& p) {
   const int quarter = p.tile_m <= 64 ? 16 : 32;
@@ -881,17 +902,19 @@ static int ln_sms(int dev) {
 }
 
 // Powers of two where K is cut, so that a program's products need few sizes.
-size_t linear_workspace_bytes(int M, int N, int K) {
-  if (ln_few(M, N, K)) return kLnHeader;
-  int dev = 0, sms = -1;
-  if (cudaGetDevice(&dev) == cudaSuccess) sms = ln_sms(dev);
-  const LnPlan p = ln_plan(M, N, K, sms > 0 ? sms : 152);
+static size_t ln_plan_bytes(const LnPlan& p) {
   if (p.split == 1) return kLnHeader;
   const size_t need =
       kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * ln_partial_rows(p) * sizeof(float);
   size_t bytes = 65536;
   while (bytes < need) bytes *= 2;
   return bytes;
+}
+size_t linear_workspace_bytes(int M, int N, int K) {
+  if (ln_few(M, N, K)) return kLnHeader;
+  int dev = 0, sms = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess) sms = ln_sms(dev);
+  return ln_plan_bytes(ln_plan_kept(M, N, K, sms > 0 ? sms : 152));
 }
 
 static LnEpilogue ln_epilogue(const Linear& l) {
@@ -955,16 +978,19 @@ static int linear_few(const Linear& l, int sms, cudaStream_t st) {
 }
 
 int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_t st) {
-  const size_t need = linear_workspace_bytes(l.M, l.N, l.K);
+  const bool few = ln_few(l.M, l.N, l.K);
+  int dev = 0, sms = -1;
+  const bool has_device = cudaGetDevice(&dev) == cudaSuccess;
+  if (has_device) sms = ln_sms(dev);
+  LnPlan p = {};
+  if (!few) p = ln_plan_kept(l.M, l.N, l.K, sms > 0 ? sms : 152);
+  const size_t need = few ? kLnHeader : ln_plan_bytes(p);
   if (workspace == nullptr || workspace_bytes < need)
     return set_last_error(FME_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (l.M == 0) return FME_OK;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return set_last_error(FME_ECUDA, "cudaGetDevice failed");
-  const int sms = ln_sms(dev);
+  if (!has_device) return set_last_error(FME_ECUDA, "cudaGetDevice failed");
   if (sms <= 0) return set_last_error(FME_ECUDA, "no SM count for device %d", dev);
-  if (ln_few(l.M, l.N, l.K)) return linear_few(l, sms, st);
-  const LnPlan p = ln_plan(l.M, l.N, l.K, sms);
+  if (few) return linear_few(l, sms, st);
   LnTcArgs a = {};
   a.e = ln_epilogue(l);
   a.rows = ln_partial_rows(p);
@@ -995,11 +1021,14 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   const bool chunked = beside > 512;
   a.tmem_cols = 32;
   while (a.tmem_cols < static_cast<uint32_t>(chunked ? 2 * a.tile_n : beside)) a.tmem_cols *= 2;
-  if (!ln_map(&a.mapx1, l.x, l.M, l.K, l.ldx, a.box_m, 0) || !ln_map(&a.mapw1, l.w, l.N, l.K, l.ldw, a.tile_n, 0) ||
-      (l.K >= kLnKBlock && (!ln_map(&a.mapx, l.x, l.M, l.K, l.ldx, a.box_m, a.slices) ||
-                            !ln_map(&a.mapw, l.w, l.N, l.K, l.ldw, a.tile_n, a.slices))))
+  // Maps for the stages that are loaded whole, and for those block by block, where there are any.
+  const bool whole = a.single > 0, blocks = a.single < a.groups;
+  if ((whole && (!ln_map(&a.mapx, l.x, l.M, l.K, l.ldx, a.box_m, a.slices) ||
+                 !ln_map(&a.mapw, l.w, l.N, l.K, l.ldw, a.tile_n, a.slices))) ||
+      (blocks && (!ln_map(&a.mapx1, l.x, l.M, l.K, l.ldx, a.box_m, 0) ||
+                  !ln_map(&a.mapw1, l.w, l.N, l.K, l.ldw, a.tile_n, 0))))
     return set_last_error(FME_ECUDA, "cuTensorMapEncodeTiled failed or unavailable");
-  if (l.K < kLnKBlock) {  // no whole block: never loaded from
+  if (!whole) {
     a.mapx = a.mapx1;
     a.mapw = a.mapw1;
   }
