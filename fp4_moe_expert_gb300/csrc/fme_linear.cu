@@ -121,34 +121,34 @@ __device__ __forceinline__ float ln_recip_approx(float d) {
 
 // Sixteen sums of one row, columns n .. n + 15: bias and activation. (The cases stand outside the loops: inside them each
 // value's code holds every case's.) BF16 outputs take exp and reciprocal by the hardware's approximations.
-__device__ __forceinline__ void ln_finish16(const LnEpilogue& e, float (&z)[16], int n) {
-  if (e.bias != nullptr && e.bias16 && n + 16 <= e.N) {
+__device__ __forceinline__ void ln_finish16(const LnEpilogue& e, const float* bias, int act, float (&z)[16], int n) {
+  if (bias != nullptr && e.bias16 && n + 16 <= e.N) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 b = __ldg(reinterpret_cast<const float4*>(e.bias + n) + i);
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n) + i);
       z[4 * i] = __fadd_rn(z[4 * i], b.x);
       z[4 * i + 1] = __fadd_rn(z[4 * i + 1], b.y);
       z[4 * i + 2] = __fadd_rn(z[4 * i + 2], b.z);
       z[4 * i + 3] = __fadd_rn(z[4 * i + 3], b.w);
     }
-  } else if (e.bias != nullptr) {
+  } else if (bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], n + i < e.N ? __ldg(e.bias + n + i) : 0.0f);
+    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], n + i < e.N ? __ldg(bias + n + i) : 0.0f);
   }
-  if (e.act == FME_ACT_NONE) return;
-  if (e.act == FME_ACT_SILU && !e.out_f32) {
+  if (act == FME_ACT_NONE) return;
+  if (act == FME_ACT_SILU && !e.out_f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = __fmul_rn(z[i], ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i]))));
-  } else if (e.act == FME_ACT_SIGMOID && !e.out_f32) {
+  } else if (act == FME_ACT_SIGMOID && !e.out_f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i])));
-  } else if (e.act == FME_ACT_RELU) {
+  } else if (act == FME_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_RELU);
-  } else if (e.act == FME_ACT_SILU) {
+  } else if (act == FME_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_SILU);
-  } else if (e.act == FME_ACT_SIGMOID) {
+  } else if (act == FME_ACT_SIGMOID) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_SIGMOID);
   } else {
@@ -157,82 +157,75 @@ __device__ __forceinline__ void ln_finish16(const LnEpilogue& e, float (&z)[16],
   }
 }
 
-// A chunk is sixteen columns (n .. n + 15, the first `cols` of them) of a warp's 32 rows (from `row`, the first `rows` of
-// them). Whole chunks of rows that start at multiples of 16 bytes are stored as the accumulator gives them, a lane a row, 32
-// or 16 bytes at a time. Others are turned through shared memory, so that neighbouring lanes store neighbouring values
-// (1533 x 895 x 3584: 16.4 us; a lane a row, value by value, 41.7).
-struct LnChunk {
-  int row, rows, n, cols;
-  bool whole;
-};
-// The residual of a chunk, asked for before its sums are read: bits of the values this lane stores.
-__device__ __forceinline__ void ln_residual(const LnEpilogue& e, const LnChunk& c, int lane, uint32_t (&raw)[16]) {
-  if (e.residual == nullptr) return;
-  if (c.whole) {
-    if (lane >= c.rows) return;
-    const size_t at = static_cast<size_t>(c.row + lane) * e.ldr + c.n;
-    uint32_t w[8];
-    if (e.out_f32) {
+// A chunk is sixteen columns of a warp's 32 rows. Whole chunks of rows that start at multiples of 16 bytes are loaded and
+// stored as the accumulator gives them, a lane a row, 32 (sector) or 16 bytes at a time.
+__device__ __forceinline__ void ln_load_whole(uint32_t (&raw)[16], const char* from, int size, bool sector) {
+  uint32_t w[8];
+  ln_ld32(from, w, sector);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ln_ld32(static_cast<const float*>(e.residual) + at + 8 * h, w, e.wide == 32);
+  for (int i = 0; i < 8; ++i) raw[i] = w[i];
+  if (size == 4) {
+    ln_ld32(from + 32, w, sector);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) raw[8 * h + i] = w[i];
-      }
-    } else {
-      ln_ld32(static_cast<const __nv_bfloat16*>(e.residual) + at, w, e.wide == 32);
+    for (int i = 0; i < 8; ++i) raw[8 + i] = w[i];
+  }
+}
+__device__ __forceinline__ void ln_add_whole(float (&z)[16], const uint32_t (&raw)[16], int size) {
+  if (size == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = w[i];
-    }
-  } else if ((lane & 15) < c.cols) {
-    const int r0 = lane >> 4;
-    const size_t at = static_cast<size_t>(c.row + r0) * e.ldr + c.n + (lane & 15);
-    if (e.out_f32) {
-      const float* from = static_cast<const float*>(e.residual) + at;
+    for (int i = 0; i < 16; ++i) z[i] = __fadd_rn(z[i], __uint_as_float(raw[i]));
+  } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (2 * i + r0 < c.rows) raw[i] = __float_as_uint(from[2 * i * e.ldr]);
-    } else {
-      const uint16_t* from = static_cast<const uint16_t*>(e.residual) + at;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (2 * i + r0 < c.rows) raw[i] = from[2 * i * e.ldr];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) raw[i] <<= 16;
+    for (int i = 0; i < 8; ++i) {
+      z[2 * i] = __fadd_rn(z[2 * i], __uint_as_float(raw[i] << 16));
+      z[2 * i + 1] = __fadd_rn(z[2 * i + 1], __uint_as_float(raw[i] & 0xFFFF0000u));
     }
   }
 }
-// Adds the residual to a chunk and stores it. z: the sums of row `lane`.
-__device__ __forceinline__ void ln_store_chunk(const LnEpilogue& e, const LnChunk& c, float (&z)[16],
-                                               const uint32_t (&raw)[16], float* turn, int lane) {
-  if (c.whole) {
-    if (lane >= c.rows) return;
-    const size_t at = static_cast<size_t>(c.row + lane) * e.ldo + c.n;
-    const bool sector = e.wide == 32;
-    uint32_t w[8];
-    if (e.out_f32) {
+__device__ __forceinline__ void ln_store_whole(const float (&z)[16], char* to, int size, bool sector) {
+  uint32_t w[8];
+  if (size == 4) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          w[i] = __float_as_uint(e.residual != nullptr ? __fadd_rn(z[8 * h + i], __uint_as_float(raw[8 * h + i]))
-                                                       : z[8 * h + i]);
-        ln_st32(static_cast<float*>(e.out) + at + 8 * h, w, sector);
-      }
-    } else {
-      if (e.residual != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[2 * i] = __fadd_rn(z[2 * i], __uint_as_float(raw[i] << 16));
-          z[2 * i + 1] = __fadd_rn(z[2 * i + 1], __uint_as_float(raw[i] & 0xFFFF0000u));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = ln_bf16x2(z[2 * i], z[2 * i + 1]);
-      ln_st32(static_cast<__nv_bfloat16*>(e.out) + at, w, sector);
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z[8 * h + i]);
+      ln_st32(to + 32 * h, w, sector);
     }
-    return;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = ln_bf16x2(z[2 * i], z[2 * i + 1]);
+    ln_st32(to, w, sector);
   }
+}
+
+// Other chunks (columns n .. n + 15, the first `cols` of them; rows from `row`, the first `rows` of them) are turned through
+// shared memory, so that neighbouring lanes store neighbouring values (1533 x 895 x 3584: 16.4 us; a lane a row, value by value,
+// 41.7).
+struct LnChunk {
+  int row, rows, n, cols;
+};
+// The residual of a chunk, asked for before its sums are read: bits of the values this lane stores.
+__device__ __forceinline__ void ln_load_turned(const LnEpilogue& e, const LnChunk& c, int lane, uint32_t (&raw)[16]) {
+  if ((lane & 15) >= c.cols) return;
+  const int r0 = lane >> 4;
+  const size_t at = static_cast<size_t>(c.row + r0) * e.ldr + c.n + (lane & 15);
+  if (e.out_f32) {
+    const float* from = static_cast<const float*>(e.residual) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + r0 < c.rows) raw[i] = __float_as_uint(from[2 * i * e.ldr]);
+  } else {
+    const uint16_t* from = static_cast<const uint16_t*>(e.residual) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + r0 < c.rows) raw[i] = from[2 * i * e.ldr];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) raw[i] <<= 16;
+  }
+}
+// Adds the residual to a chunk and stores it. z: the sums of row `lane`.
+__device__ __forceinline__ void ln_store_turned(const LnEpilogue& e, const LnChunk& c, float (&z)[16],
+                                                const uint32_t (&raw)[16], float* turn, int lane) {
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 16; ++i) turn[lane * 17 + i] = z[i];
@@ -641,6 +634,11 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     // Of 128 rows a warp's lanes hold 32; of 64 rows the first 16 of its lanes hold 16.
     const int each_quad = a.half_m ? 16 : 32;
     float* turn = S.turn[warp];
+    const float* bias = a.e.bias;
+    const int size = CHUNKED || a.e.out_f32 ? 4 : 2, wide = a.e.wide, act = a.e.act;
+    // (The branches' likelihoods place the code of activations and of ragged chunks behind the loop, which then runs on without
+    // jumps: 300 x 7168 x 2048 13.2 -> 12.7 us, 64 x 7168 x 2048 7.0 -> 6.8.)
+    const bool more = bias != nullptr || act != FME_ACT_NONE;
     uint32_t n = 0;
     bool ok = true;
     for (int u = first; u < a.units && ok; u += step) {
@@ -662,15 +660,6 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         ++n;
       };
       // This thread's column chunks: 32 i + 16 half.
-      auto chunk = [&](int c) {
-        LnChunk k;
-        k.row = m0 + each_quad * quad;
-        k.rows = rows;
-        k.n = n0 + c + 16 * half;
-        k.cols = min(16, a.e.N - k.n);
-        k.whole = a.e.wide != 0 && k.cols == 16;
-        return k;
-      };
       auto has = [&](int c) { return c + 16 * half < a.tile_n && n0 + c + 16 * half < a.e.N; };
       if (CHUNKED) {
         // The accumulations' sums meet in registers, 16 columns 32 i + 16 half each; the tile's go back over the last one's.
@@ -742,40 +731,58 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         }
         mine = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(a.split) - 1u;
       }
-      if (mine) {
-        for (int c = 0; has(c); c += 32) {
-          const LnChunk k = chunk(c);
-          uint32_t raw[16];
-          ln_residual(a.e, k, lane, raw);
-          float z[16];
-          if (a.split == 1) {
-            sums(c, z);
-          } else {
-            // In K's order, four units' partial sums on their way at once; lanes past the rows read the last row's.
-            const float4* from = tile + (c / 4) * 32 - max(lane - (rows - 1), 0);
+      auto join = [&](int c, float (&z)[16]) {
+        if (a.split == 1) {
+          sums(c, z);
+          return;
+        }
+        // In K's order, JOIN units' partial sums on their way at once; lanes past the rows read the last row's.
+        const float4* from = tile + (c / 4) * 32 - max(lane - (rows - 1), 0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
 #pragma unroll 1
-            for (int s = 0; s < a.split; s += JOIN, from += JOIN * (each / 4)) {
-              float4 p[JOIN][4];
+        for (int s = 0; s < a.split; s += JOIN, from += JOIN * (each / 4)) {
+          float4 p[JOIN][4];
 #pragma unroll
-              for (int b = 0; b < JOIN; ++b)
+          for (int b = 0; b < JOIN; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  p[b][i] = s + b < a.split ? __ldcg(from + b * (each / 4) + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i)
+              p[b][i] = s + b < a.split ? __ldcg(from + b * (each / 4) + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-              for (int b = 0; b < JOIN; ++b)
+          for (int b = 0; b < JOIN; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  z[4 * i] = __fadd_rn(z[4 * i], p[b][i].x);
-                  z[4 * i + 1] = __fadd_rn(z[4 * i + 1], p[b][i].y);
-                  z[4 * i + 2] = __fadd_rn(z[4 * i + 2], p[b][i].z);
-                  z[4 * i + 3] = __fadd_rn(z[4 * i + 3], p[b][i].w);
-                }
+            for (int i = 0; i < 4; ++i) {
+              z[4 * i] = __fadd_rn(z[4 * i], p[b][i].x);
+              z[4 * i + 1] = __fadd_rn(z[4 * i + 1], p[b][i].y);
+              z[4 * i + 2] = __fadd_rn(z[4 * i + 2], p[b][i].z);
+              z[4 * i + 3] = __fadd_rn(z[4 * i + 3], p[b][i].w);
             }
+        }
+      };
+      if (mine) {
+        const size_t row = m0 + each_quad * quad + lane, col = n0 + 16 * half;
+        char* to = static_cast<char*>(a.e.out) + (row * a.e.ldo + col) * size;
+        const char* from =
+            a.e.residual == nullptr ? nullptr : static_cast<const char*>(a.e.residual) + (row * a.e.ldr + col) * size;
+        for (int c = 0; has(c); c += 32) {
+          const LnChunk k = {m0 + each_quad * quad, rows, n0 + c + 16 * half, min(16, a.e.N - n0 - c - 16 * half)};
+          const bool whole = wide != 0 && k.cols == 16;
+          uint32_t raw[16];
+          if (from != nullptr) {
+            if (__builtin_expect(!whole, 0))
+              ln_load_turned(a.e, k, lane, raw);
+            else if (lane < rows)
+              ln_load_whole(raw, from + c * size, size, wide == 32);
           }
-          ln_finish16(a.e, z, k.n);
-          ln_store_chunk(a.e, k, z, raw, turn, lane);
+          float z[16];
+          join(c, z);
+          if (__builtin_expect(more, 0)) ln_finish16(a.e, bias, act, z, k.n);
+          if (__builtin_expect(whole, 1)) {
+            if (from != nullptr) ln_add_whole(z, raw, size);
+            if (lane < rows) ln_store_whole(z, to + c * size, size, wide == 32);
+          } else {
+            ln_store_turned(a.e, k, z, raw, turn, lane);
+          }
         }
       }
       release();
