@@ -23,17 +23,17 @@
 //   off. Accumulations of about kLnChunk blocks are added with rounding instead: 5e-7. They stand side by side in tensor memory
 //   where a unit's fit (128 x 256 x 7168 9.2 -> 7.8 us), else they are added in registers as they end (CHUNKED: 16384 x 256 x
 //   7168 57.5 us, the chain 53.8). BF16 outputs, whose rounding is 250 times that, take the chain.
-// What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB) and
-// read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
+// What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB)
+// and read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
 // burst; 615 to 640 at the power limit. The tiles' order counts: 771 us with the row tiles of one weight tile one after
 // another). Small tiles the same: an MMA reads its 128 (up to 64 tokens: 64) token rows whatever it has of them, so one of
-// 48 columns takes 70 clocks as one of 256 takes 190 (64 x 7168 x 2048: 8.1 us with 128 rows, 7.0 with 64). Measured and left out: 256 x 256 tiles, two accumulators that share the weights, with three
-// stages of 64 KB (626 us against 577) and with six of half as many values (809: TMA takes rows of 64 bytes no faster than
-// rows of 128); prefetches into L2 ahead of the ring (router of 16384 tokens 57.8 against 57.4 us, 64 x 4096 x 7168 18.1
-// against 17.4); CTAs that start at different places of K (no difference); two CTAs an SM with half the ring (64 x 7168 x
-// 2048 11.2 us against 9.1); partial sums with a row's columns together (512 x 256 x 7168 17 us against 12.5).
-// Rows whose stride is an odd multiple of 16 bytes cost more: 128 bytes of a row then lie in five sectors (1533 x 895 x 3581
-// 22.8 us, with strides of whole sectors 17.3).
+// 48 columns takes 70 clocks as one of 256 takes 190 (64 x 7168 x 2048: 8.1 us with 128 rows, 7.0 with 64). Measured and
+// left out: 256 x 256 tiles, two accumulators that share the weights, with three stages of 64 KB (626 us against 577) and
+// with six of half as many values (809: TMA takes rows of 64 bytes no faster than rows of 128); prefetches into L2 ahead of
+// the ring (router of 16384 tokens 57.8 against 57.4 us, 64 x 4096 x 7168 18.1 against 17.4); CTAs that start at different
+// places of K (no difference); two CTAs an SM with half the ring (64 x 7168 x 2048 11.2 us against 9.1); partial sums with a
+// row's columns together (512 x 256 x 7168 17 us against 12.5). Rows whose stride is an odd multiple of 16 bytes cost more:
+// 128 bytes of a row then lie in five sectors (1533 x 895 x 3581 22.8 us, with strides of whole sectors 17.3).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

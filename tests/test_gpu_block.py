@@ -108,6 +108,28 @@ def test_linear_is_the_same_bits_every_time(fme):
             assert torch.equal(ref, fme.linear_bf16(x, w, out_dtype=torch.float32))
 
 
+def test_linear_cut_products_of_one_workspace(fme):
+    """FP32 sums in one and several accumulations, K cut and not, ragged and residual, in turn on one workspace."""
+    shapes = [(17, 256, 7168), (512, 256, 7168), (129, 250, 6999), (2048, 256, 7168), (70, 3000, 4096), (300, 896, 3584),
+              (64, 48, 16384)]
+    ws = fme.Workspace(max(fme.linear_bf16_workspace(*shape) for shape in shapes), DEV)
+    first = {}
+    for again in range(2):
+        for i, (M, N, K) in enumerate(shapes):
+            for f32 in (True, False):
+                out = _check_linear(fme, M, N, K, i % 2 == 0, ACTS[i % 5], i % 3 != 0, f32, ws=ws) if not again else None
+                x, w = (torch.ones(n, (K + 7) // 8 * 8, device=DEV, dtype=BF)[:, :K] for n in (M, N))
+                x[::3] = 0.5
+                y = fme.linear_bf16(x, w, out_dtype=torch.float32, workspace=ws)
+                assert torch.equal(y, x[:, :1].float() * K * torch.ones(1, N, device=DEV))
+                if out is not None:
+                    first[M, N, K, f32] = out
+                else:
+                    out = _check_linear(fme, M, N, K, i % 2 == 0, ACTS[i % 5], i % 3 != 0, f32, ws=ws)
+                    assert torch.equal(first[M, N, K, f32], out)
+    assert ws.error() == 0
+
+
 def test_linear_reports_a_workspace_that_was_not_cleared(fme):
     M, N, K = 64, 256, 7168  # K is cut: units count their arrivals in the workspace
     x, w = torch.randn(M, K, device=DEV).to(BF), torch.randn(N, K, device=DEV).to(BF)
