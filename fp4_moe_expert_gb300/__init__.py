@@ -125,8 +125,9 @@ def _need(t, dtype, shape, name, device=None):
 
 
 class Workspace:
-    """Caller-owned device scratch for one stream: zero-filled once at creation;
-    every successful call leaves it zeroed again."""
+    """Caller-owned device scratch for one stream: zero-filled once at creation; every successful call leaves the words
+    that the next one of its kind needs zero. Routing, the grouped products and linear_bf16 may share one of the largest
+    need; the decode calls (routed with layer, shared expert, NVFP4) take one for each kind and its sizes other than M."""
 
     def __init__(self, nbytes, device):
         self.nbytes = int(nbytes)

@@ -22,6 +22,12 @@ bool ensure_smem_attr(int dev, const void* kernel, size_t bytes);
 // override, default 1000 ms).
 unsigned long long wait_timeout_ns();
 
+// Workspaces of the operators of any number of tokens (routing, grouped products, dense product): the words that a call must
+// find zero, and leaves so, lie in these first bytes, each operator's in places of its own (byte 0: the error word of all; 64:
+// routing's meeting; 256 to the end: the dense product's counts), and what need not be zero lies behind them. So one workspace
+// may serve them all in turn.
+constexpr size_t kWorkspaceWords = 4096;
+
 size_t nvfp4_workspace_bytes(int M, int H, int N, int L, int top_k);
 
 // The routed experts of one FP8 layer call (E == 0: none).

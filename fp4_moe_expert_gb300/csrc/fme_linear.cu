@@ -416,8 +416,8 @@ constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows
 constexpr int kLnStageBytes = 65536;
 constexpr int kLnChunk = 8;
 constexpr int kLnGroup = 8;                // weight tiles that are walked together
-constexpr int kLnHeader = 4096;            // workspace: error word, then from byte 256 the arrival counters of cut tiles
-static_assert(256 + kLnMaxUnits / 2 * kLnEpiWarps * 4 <= kLnHeader, "a tile that is cut has two units at least");
+constexpr int kLnCounts = 256;             // byte of the workspace where the arrival counters of cut tiles begin
+static_assert(kLnCounts + kLnMaxUnits / 2 * kLnEpiWarps * 4 <= kWorkspaceWords, "a tile that is cut has two units at least");
 
 struct LnTcArgs {
   CUtensorMap mapx, mapx1;  // x [M, K], box box_m rows x 64 values, `slices` (1) K blocks of them
@@ -912,15 +912,15 @@ static int ln_sms(int dev) {
 
 // Powers of two where K is cut, so that a program's products need few sizes.
 static size_t ln_plan_bytes(const LnPlan& p) {
-  if (p.split == 1) return kLnHeader;
-  const size_t need =
-      kLnHeader + static_cast<size_t>(p.tiles_m) * p.tiles_n * p.split * p.tile_n * ln_partial_rows(p) * sizeof(float);
+  if (p.split == 1) return kWorkspaceWords;
+  const size_t part = static_cast<size_t>(p.tile_n) * ln_partial_rows(p) * sizeof(float);  // of a unit
+  const size_t need = kWorkspaceWords + part * p.tiles_m * p.tiles_n * p.split;
   size_t bytes = 65536;
   while (bytes < need) bytes *= 2;
   return bytes;
 }
 size_t linear_workspace_bytes(int M, int N, int K) {
-  if (ln_few(M, N, K)) return kLnHeader;
+  if (ln_few(M, N, K)) return kWorkspaceWords;
   int dev = 0, sms = -1;
   if (cudaGetDevice(&dev) == cudaSuccess) sms = ln_sms(dev);
   return ln_plan_bytes(ln_plan_kept(M, N, K, sms > 0 ? sms : 152));
@@ -993,7 +993,7 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
   if (has_device) sms = ln_sms(dev);
   LnPlan p = {};
   if (!few) p = ln_plan_kept(l.M, l.N, l.K, sms > 0 ? sms : 152);
-  const size_t need = few ? kLnHeader : ln_plan_bytes(p);
+  const size_t need = few ? kWorkspaceWords : ln_plan_bytes(p);
   if (workspace == nullptr || workspace_bytes < need)
     return set_last_error(FME_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (l.M == 0) return FME_OK;
@@ -1042,8 +1042,8 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
     a.mapw = a.mapw1;
   }
   a.err = static_cast<uint32_t*>(workspace);
-  a.arrived = a.err + 64;
-  a.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + kLnHeader);
+  a.arrived = a.err + kLnCounts / 4;
+  a.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + kWorkspaceWords);
   a.timeout_ns = wait_timeout_ns();
   const void* kernel = reinterpret_cast<const void*>(chunked ? linear_tc_kernel<true> : linear_tc_kernel<false>);
   if (!ensure_smem_attr(dev, kernel, kLnSmemBytes)) return FME_ECUDA;

@@ -689,7 +689,7 @@ static int rt_ctas(int T) {
 static int rt_pitch(int E) { return (E + 7) & ~7; }
 
 size_t route_workspace_bytes(int T, int E) {
-  return 256 + ((static_cast<size_t>(rt_ctas(T)) * rt_pitch(E) * sizeof(uint16_t) + 255) & ~size_t(255));
+  return kWorkspaceWords + ((static_cast<size_t>(rt_ctas(T)) * rt_pitch(E) * sizeof(uint16_t) + 255) & ~size_t(255));
 }
 
 int route(const void* logits, int logits_dtype, const float* bias, int T, int E, int top_k, const RouteScores* scored,
@@ -737,7 +737,7 @@ int route(const void* logits, int logits_dtype, const float* bias, int T, int E,
   a.tokens = tokens;
   a.err = static_cast<uint32_t*>(workspace);
   a.sync = a.err + 16;
-  a.counts = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + 256);
+  a.counts = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWorkspaceWords);
   a.timeout_ns = wait_timeout_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));

@@ -25,7 +25,10 @@
  *   order, including calls with fewer tokens M than it was sized for (same
  *   other sizes). fme_moe_routed_fp8 and fme_moe_layer_fp8 calls with the same
  *   H, I, E and top_k may share one workspace (sized for the larger need);
- *   the shared-expert and NVFP4 calls each need their own. Two calls that
+ *   the shared-expert and NVFP4 calls each need their own. Calls of
+ *   fme_moe_route, fme_moe_route_groups, the grouped products and
+ *   fme_linear_bf16, of any sizes, may share one workspace of the largest
+ *   need, but not with the decode calls named before. Two calls that
  *   overlap on the GPU need two workspaces. After a device-side error, clear
  *   it again before reuse.
  * - BF16 is IEEE bfloat16 (uint16 bit patterns). FP8 is E4M3 ("e4m3fn": no
