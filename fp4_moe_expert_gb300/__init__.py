@@ -149,12 +149,14 @@ class Workspace:
 _ws_cache = {}
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, *layout):
+    """The caller's workspace, or one kept per device, size and `layout`: the kind of call and what its counters' places
+    hang on, so that no call gets one that another kind's data lies in."""
     if workspace is not None:
         if workspace.nbytes < nbytes:
             raise ValueError(f"workspace of {workspace.nbytes} bytes, {nbytes} needed")
         return workspace
-    key = (device.index if device.index is not None else torch.cuda.current_device(), nbytes)
+    key = (device.index if device.index is not None else torch.cuda.current_device(), nbytes, layout)
     ws = _ws_cache.get(key)
     if ws is None:
         ws = Workspace(nbytes, device)
@@ -215,7 +217,7 @@ def moe_routed_fp8(x, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0
     if weights is None:
         weights = torch.empty(M, top_k, dtype=torch.float32, device=dev)
     need = moe_routed_fp8_workspace(M, H, I, E, top_k)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "routed", H, I, E, top_k)
     ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
     _check(lib.fme_moe_routed_fp8(_ptr(x), _ptr(logits), ldt, _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
                                   _ptr(s2), M, H, I, E, top_k, float(limit), float(scale), int(bool(ue8m0)),
@@ -253,7 +255,7 @@ def moe_routed_fp8_mx(xq, xscales, logits, bias, w13, s13, w2, s2, top_k, limit,
     if weights is None:
         weights = torch.empty(M, top_k, dtype=torch.float32, device=dev)
     need = moe_routed_fp8_workspace(M, H, I, E, top_k)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "routed", H, I, E, top_k)
     _check(lib.fme_moe_routed_fp8_mx(_ptr(xq), _ptr(xscales), _ptr(logits), dt, _ptr(bias), _ptr(w13), _ptr(s13),
                                      _ptr(w2), _ptr(s2), M, H, I, E, top_k, float(limit), float(scale), int(ue8m0),
                                      _ptr(out), _ptr(ids), _ptr(weights), ws.ptr(), ws.nbytes, _stream(dev)))
@@ -283,7 +285,7 @@ def shared_expert_fp8(x, w13, s13, w2, s2, limit, ue8m0, out=None, gate_up=None,
     if want_gate_up and gate_up is None:
         gate_up = torch.empty(M, 2 * I, dtype=torch.bfloat16, device=dev)
     need = shared_expert_fp8_workspace(M, H, I)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "shared", H, I)
     _check(lib.fme_shared_expert_fp8(_ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), M, H, I, float(limit),
                                      int(bool(ue8m0)), _ptr(gate_up), _ptr(out), ws.ptr(), ws.nbytes,
                                      _stream(dev)))
@@ -328,7 +330,7 @@ def moe_layer_fp8(x, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
     if shared_out is None:
         shared_out = torch.empty(M, H, dtype=torch.bfloat16, device=dev)
     need = moe_layer_fp8_workspace(M, H, I, E, top_k)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "layer", H, I, E, top_k)
     ldt = FME_F32 if logits.dtype == torch.float32 else FME_BF16
     _check(lib.fme_moe_layer_fp8(_ptr(x), _ptr(logits), ldt, _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
                                  _ptr(s2), M, H, I, E, top_k, float(limit), float(scale), int(bool(ue8m0)),
@@ -852,7 +854,7 @@ def moe_routed_nvfp4(x, topk_ids, topk_weights, w13, s13, w2, s2, e0, limit=floa
     if y is None:
         y = torch.empty(M, H, dtype=torch.bfloat16, device=dev)
     need = moe_routed_nvfp4_workspace(M, H, N, L, top_k)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "nvfp4", H, N, L)
     _check(lib.fme_moe_routed_nvfp4(_ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(w2),
                                     _ptr(s2), M, H, N, L, int(e0), top_k, float(limit), _ptr(y), ws.ptr(),
                                     ws.nbytes, _stream(dev)))
@@ -887,7 +889,7 @@ def moe_layer_nvfp4(x, logits, bias, w13, s13, w2, s2, e0, top_k, scale=1.0, lim
     ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
     weights = torch.empty(M, top_k, dtype=torch.float32, device=dev)
     need = moe_routed_nvfp4_workspace(M, H, N, L, top_k)
-    ws = _workspace(need, dev, workspace)
+    ws = _workspace(need, dev, workspace, "nvfp4", H, N, L)
     _check(lib.fme_moe_layer_nvfp4(_ptr(x), _ptr(logits), dt, _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
                                    M, H, N, L, E, int(e0), int(top_k), float(scale), float(limit), _ptr(y),
                                    _ptr(ids), _ptr(weights), ws.ptr(), ws.nbytes, _stream(dev)))
