@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
           if (before >= static_cast<uint32_t>(a.split)) atomicOr(a.err, kErrCrossWait);
         }
         mine = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(a.split) - 1u;
+        __syncwarp();  // the other lanes' reads of the parts stand behind lane 0's acquire (a shuffle orders no memory)
       }
       auto join = [&](int c, float (&z)[16]) {
         if (a.split == 1) {
