@@ -416,8 +416,11 @@ constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows
 constexpr int kLnStageBytes = 65536;
 constexpr int kLnChunk = 8;
 constexpr int kLnGroup = 8;                // weight tiles that are walked together
-constexpr int kLnCounts = 256;             // byte of the workspace where the arrival counters of cut tiles begin
-static_assert(kLnCounts + kLnMaxUnits / 2 * kLnEpiWarps * 4 <= kWorkspaceWords, "a tile that is cut has two units at least");
+constexpr int kLnCountsAt = 256;           // byte of the workspace where the counts of cut tiles begin, one a warp of a tile
+constexpr int kLnCounts = kLnMaxUnits / 2 * kLnEpiWarps;  // (a tile that is cut has two units at least)
+constexpr uint32_t kLnBegun = 1u << 16;    // a count: units begun, and in the lower half arrived
+constexpr uint32_t kLnRefused = 1u << 31;  // in every count: products that cut K write nothing until the workspace is cleared
+static_assert(kLnCountsAt + kLnCounts * 4 <= kWorkspaceWords, "counts");
 
 struct LnTcArgs {
   CUtensorMap mapx, mapx1;  // x [M, K], box box_m rows x 64 values, `slices` (1) K blocks of them
@@ -435,7 +438,7 @@ struct LnTcArgs {
   float4* partial;     // [units][rows / 32][tile_n / 4][32] of four columns
   int rows;            // rows of a partial tile: 32 a quarter
   uint32_t* err;
-  uint32_t* arrived;  // [tiles][warps], zero between calls
+  uint32_t* counts;  // [tiles][warps], zero between calls
   unsigned long long timeout_ns;
   LnEpilogue e;
 };
@@ -472,6 +475,18 @@ __device__ __forceinline__ uint32_t ln_arrive(uint32_t* counter) {
   uint32_t before;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
   return before;
+}
+
+// Counts that are incomplete, or of no call, would let a later call take a unit for the last one too early.
+__device__ __forceinline__ void ln_refuse(uint32_t* counts) {
+#pragma unroll 1
+  for (int i = 0; i < kLnCounts; ++i) atomicOr(counts + i, kLnRefused);
+}
+// This CTA leaves its units undone.
+__device__ __forceinline__ void ln_give_up(const LnTcArgs& a, LnShared& S) {
+  S.abort = 1;
+  atomicOr(a.err, kErrRingWait);
+  if (a.split > 1) ln_refuse(a.counts);
 }
 
 struct LnUnit {
@@ -575,10 +590,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         if (ok) ok = mbar_wait_spin(&S.done[k % n], (k / n) & 1, a.timeout_ns, abort);
         if (!ok) mbar_wait_spin(&S.full[k % n], (k / n) & 1, 10000000ull, nullptr);
       }
-      if (!ok) {
-        atomicOr(a.err, kErrRingWait);
-        S.abort = 1;
-      }
+      if (!ok) ln_give_up(a, S);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -622,8 +634,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       }
     }
     if (!ok && elect_one()) {
-      atomicOr(a.err, kErrRingWait);
-      S.abort = 1;
+      ln_give_up(a, S);
       tc_commit(&S.drain);
       if (!mbar_wait_spin(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
     }
@@ -647,6 +658,13 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       const LnUnit t = ln_unit(a, u);
       const int m0 = a.tile_m * t.m, n0 = a.tile_n * t.n;
       const int rows = min(each_quad, min(a.tile_m, a.e.M - m0) - each_quad * quad);  // of this warp
+      // A warp's count of a cut tile: begun is counted here, long before the result is needed, arrived where its part is stored.
+      // So at any moment no more have arrived than begun and no more begun than there are units, and a count that no call left
+      // shows, if not to the unit that begins first then to one that finds too many begun. (64 x 256 x 7168 FP32 6.75 -> 6.85
+      // us, 300 x 896 x 3584 10.1 -> 10.35; with a mark of its own that every warp reads, one address for all, 7.1 and 10.4.)
+      uint32_t* const count = a.counts + t.tile * kLnEpiWarps + warp;
+      uint32_t begun = 0, before = 0;
+      if (a.split > 1 && rows > 0 && lane == 0) begun = atomicAdd(count, kLnBegun);
       uint32_t base = 0;  // this thread's row of the accumulator, from the columns of its half
       auto wait = [&]() {
         ok = mbar_wait_spin(&S.tfull[n & 1], (n >> 1) & 1, a.timeout_ns, abort);
@@ -723,15 +741,8 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
           }
         }
         __syncwarp();
-        uint32_t before = 0;
-        if (lane == 0) {
-          uint32_t* arrived = a.arrived + t.tile * kLnEpiWarps + warp;
-          before = ln_arrive(arrived);
-          if (before == static_cast<uint32_t>(a.split) - 1u) *arrived = 0u;
-          // A count that no call left: the tile may have no last unit, or one too early.
-          if (before >= static_cast<uint32_t>(a.split)) atomicOr(a.err, kErrCrossWait);
-        }
-        mine = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(a.split) - 1u;
+        if (lane == 0 && begun < kLnRefused) before = ln_arrive(count);
+        mine = __shfl_sync(0xFFFFFFFFu, before, 0) == a.split * kLnBegun + a.split - 1u;
         __syncwarp();  // the other lanes' reads of the parts stand behind lane 0's acquire (a shuffle orders no memory)
       }
       auto join = [&](int c, float (&z)[16]) {
@@ -789,11 +800,20 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         }
       }
       release();
+      if (a.split > 1 && rows > 0 && lane == 0) {
+        const uint32_t n = a.split;
+        if (mine) atomicAnd(count, kLnRefused);
+        if (begun >= kLnRefused) {
+          atomicOr(a.err, kErrCrossWait);
+          atomicSub(count, kLnBegun);
+        } else if (begun / kLnBegun >= n || begun % kLnBegun > begun / kLnBegun || before / kLnBegun > n ||
+                   before % kLnBegun >= before / kLnBegun) {
+          atomicOr(a.err, kErrCrossWait);
+          ln_refuse(a.counts);
+        }
+      }
     }
-    if (!ok && lane == 0) {
-      atomicOr(a.err, kErrRingWait);
-      S.abort = 1;
-    }
+    if (!ok && lane == 0) ln_give_up(a, S);
     __syncwarp();
   }
   tc_fence_before();
@@ -1043,7 +1063,7 @@ int linear(const Linear& l, void* workspace, size_t workspace_bytes, cudaStream_
     a.mapw = a.mapw1;
   }
   a.err = static_cast<uint32_t*>(workspace);
-  a.arrived = a.err + kLnCounts / 4;
+  a.counts = a.err + kLnCountsAt / 4;
   a.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + kWorkspaceWords);
   a.timeout_ns = wait_timeout_ns();
   const void* kernel = reinterpret_cast<const void*>(chunked ? linear_tc_kernel<true> : linear_tc_kernel<false>);

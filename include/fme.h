@@ -595,8 +595,11 @@ int fme_block_norm(const void* x, long long ldx, const float* route_weights, int
  *   refused. The workspace (fme_linear_bf16_workspace) must be zeroed before
  *   its first use; it serves every product that needs no more. Errors:
  *   FME_OK, FME_EINVAL, FME_EALIGN, FME_EWORKSPACE, FME_ECUDA; device waits
- *   that gave up set error bits 1 and 4 of the workspace, counters that no call
- *   left (a workspace that was not cleared) bit 2.
+ *   that gave up set error bits 1 and 4 of the workspace, counts that no call
+ *   left (a workspace that was not cleared) bit 2; the call's output is then not
+ *   valid. Every later product of this workspace that cuts K (those whose
+ *   workspace is above 4096 bytes) sets bit 2 and writes nothing until the
+ *   workspace is cleared: reading the error word does not clear the counts.
  */
 int fme_linear_bf16(const void* x, long long ldx, const void* w, long long ldw, const float* bias, int activation,
                     const void* residual, long long ldr, int M, int N, int K, void* out, int out_dtype, long long ldo,
