@@ -754,12 +754,20 @@ def moe_grouped_gemm_fp8(a, sa, w, sw, offsets, in_rows=None, out_rows=None, out
     return out
 
 
-def moe_prompt_workspaces(T, H, I, E, top_k, device):
-    """The workspaces of moe_prompt_fp8 (routing, gate/up and down product) for up to T tokens."""
+def _most_linear_bytes(T, N, K):
+    """The most that linear_bf16_workspace wants of any product of up to T tokens: fewer tokens, whose K is cut, may need
+    more than many. (K is cut where the tiles, of more than 64 tokens, are fewer than SMs: up to 10240 tokens.)"""
+    return max(linear_bf16_workspace(t, N, K) for t in range(min(T, 1), min(T, 10240) + 1))
+
+
+def moe_prompt_workspaces(T, H, I, E, top_k, device, router=False):
+    """The workspaces of moe_prompt_fp8 (routing, gate/up and down product) for up to T tokens, and with `router` a fourth
+    one for the router's product of moe_prompt_block_fp8."""
     R = T * top_k
-    return (Workspace(moe_route_workspace(T, E, top_k), device),
-            Workspace(moe_grouped_fp8_workspace(R, H, 2 * I, E), device),
-            Workspace(moe_grouped_fp8_workspace(R, I, H, E), device))
+    ws = (Workspace(moe_route_workspace(T, E, top_k), device),
+          Workspace(moe_grouped_fp8_workspace(R, H, 2 * I, E), device),
+          Workspace(moe_grouped_fp8_workspace(R, I, H, E), device))
+    return (*ws, Workspace(_most_linear_bytes(T, E, H), device)) if router else ws
 
 
 def _need_prompt(xq, sx, logits, bias, w13, w2, shared_out=None):
@@ -821,9 +829,12 @@ def moe_prompt_block_fp8(xq, sx, normed, residual, router, bias, w13, s13, w2, s
     for the next block (next_gamma, quant).
 
     xq, sx, normed [T, H] and residual [T, H] as add_rmsnorm_fp8 or block_norm return them (quant "fp8", with normed);
-    the rest as moe_prompt_fp8 and block_norm. Returns (q, scales, residual_out, normed, ids, weights): what the next
+    the rest as moe_prompt_fp8 and block_norm, and of workspaces a fourth one may serve the router's product
+    (moe_prompt_workspaces with router=True; without it that product has one of the binding's, and its errors are not
+    among the caller's). Returns (q, scales, residual_out, normed, ids, weights): what the next
     block takes (q, scales and normed None where not asked for: normed comes with next_gamma), and the routing."""
-    logits = linear_bf16(normed, router, out_dtype=torch.float32)
+    own = workspaces[3] if workspaces and len(workspaces) > 3 else None
+    logits = linear_bf16(normed, router, out_dtype=torch.float32, workspace=own)
     rows, ids, weights = moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
                                              workspaces, score, groups, top_groups, group_top, renormalise)
     return (*block_norm(rows, next_gamma, residual, weights, shared_out, post_gamma, gate, residual_scale, eps, quant,
