@@ -477,18 +477,6 @@ __device__ __forceinline__ uint32_t ln_arrive(uint32_t* counter) {
   return before;
 }
 
-// Counts that are incomplete, or of no call, would let a later call take a unit for the last one too early.
-__device__ __forceinline__ void ln_refuse(uint32_t* counts) {
-#pragma unroll 1
-  for (int i = 0; i < kLnCounts; ++i) atomicOr(counts + i, kLnRefused);
-}
-// This CTA leaves its units undone.
-__device__ __forceinline__ void ln_give_up(const LnTcArgs& a, LnShared& S) {
-  S.abort = 1;
-  atomicOr(a.err, kErrRingWait);
-  if (a.split > 1) ln_refuse(a.counts);
-}
-
 struct LnUnit {
   int m, n, tile, g0, g1;  // tile, and the unit's stages of K
 };
@@ -590,7 +578,10 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         if (ok) ok = mbar_wait_spin(&S.done[k % n], (k / n) & 1, a.timeout_ns, abort);
         if (!ok) mbar_wait_spin(&S.full[k % n], (k / n) & 1, 10000000ull, nullptr);
       }
-      if (!ok) ln_give_up(a, S);
+      if (!ok) {
+        atomicOr(a.err, kErrRingWait);
+        S.abort = 1;
+      }
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -634,7 +625,8 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
       }
     }
     if (!ok && elect_one()) {
-      ln_give_up(a, S);
+      atomicOr(a.err, kErrRingWait);
+      S.abort = 1;
       tc_commit(&S.drain);
       if (!mbar_wait_spin(&S.drain, 0, a.timeout_ns, nullptr)) atomicOr(a.err, kErrDrain);
     }
@@ -653,17 +645,18 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
     // jumps: 300 x 7168 x 2048 13.2 -> 12.7 us, 64 x 7168 x 2048 7.0 -> 6.8.)
     const bool more = bias != nullptr || act != FME_ACT_NONE;
     uint32_t n = 0;
-    bool ok = true;
+    bool ok = true, refuse = false;
     for (int u = first; u < a.units && ok; u += step) {
       const LnUnit t = ln_unit(a, u);
       const int m0 = a.tile_m * t.m, n0 = a.tile_n * t.n;
       const int rows = min(each_quad, min(a.tile_m, a.e.M - m0) - each_quad * quad);  // of this warp
       // A warp's count of a cut tile: begun is counted here, long before the result is needed, arrived where its part is stored.
       // So at any moment no more have arrived than begun and no more begun than there are units, and a count that no call left
-      // shows, if not to the unit that begins first then to one that finds too many begun. (64 x 256 x 7168 FP32 6.75 -> 6.85
-      // us, 300 x 896 x 3584 10.1 -> 10.35; with a mark of its own that every warp reads, one address for all, 7.1 and 10.4.)
+      // shows, if not to the unit that begins first then to one that finds too many begun. (300 x 896 x 3584 FP32 10.2 -> 10.3
+      // us, 20 x 16 x 3584 4.9 -> 5.1, 64 x 256 x 7168 FP32 6.75 either way and, with a mark of its own that every warp reads,
+      // one address for all, 7.1.)
       uint32_t* const count = a.counts + t.tile * kLnEpiWarps + warp;
-      uint32_t begun = 0, before = 0;
+      uint32_t begun = 0;
       if (a.split > 1 && rows > 0 && lane == 0) begun = atomicAdd(count, kLnBegun);
       uint32_t base = 0;  // this thread's row of the accumulator, from the columns of its half
       auto wait = [&]() {
@@ -741,7 +734,19 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
           }
         }
         __syncwarp();
-        if (lane == 0 && begun < kLnRefused) before = ln_arrive(count);
+        uint32_t before = 0;
+        if (lane == 0) {
+          const uint32_t n = a.split;
+          if (begun < kLnRefused) {
+            before = ln_arrive(count);
+            if (before == n * kLnBegun + n - 1u) atomicAnd(count, kLnRefused);
+            refuse = begun / kLnBegun >= n || begun % kLnBegun > begun / kLnBegun || before / kLnBegun > n ||
+                     before % kLnBegun >= before / kLnBegun;
+          } else {
+            atomicOr(a.err, kErrCrossWait);
+            atomicSub(count, kLnBegun);
+          }
+        }
         mine = __shfl_sync(0xFFFFFFFFu, before, 0) == a.split * kLnBegun + a.split - 1u;
         __syncwarp();  // the other lanes' reads of the parts stand behind lane 0's acquire (a shuffle orders no memory)
       }
@@ -800,20 +805,14 @@ __global__ void __launch_bounds__(kLnThreads, 1) linear_tc_kernel(const __grid_c
         }
       }
       release();
-      if (a.split > 1 && rows > 0 && lane == 0) {
-        const uint32_t n = a.split;
-        if (mine) atomicAnd(count, kLnRefused);
-        if (begun >= kLnRefused) {
-          atomicOr(a.err, kErrCrossWait);
-          atomicSub(count, kLnBegun);
-        } else if (begun / kLnBegun >= n || begun % kLnBegun > begun / kLnBegun || before / kLnBegun > n ||
-                   before % kLnBegun >= before / kLnBegun) {
-          atomicOr(a.err, kErrCrossWait);
-          ln_refuse(a.counts);
-        }
-      }
     }
-    if (!ok && lane == 0) ln_give_up(a, S);
+    if (__any_sync(0xFFFFFFFFu, !ok || refuse)) {
+      if (!ok) S.abort = 1;
+      if (lane == 0) atomicOr(a.err, ok ? kErrCrossWait : kErrRingWait);
+      // Counts that stay incomplete, or are of no call, would let a later call take a unit for the last one too early.
+#pragma unroll 1
+      for (int i = lane; a.split > 1 && i < kLnCounts; i += 32) atomicOr(a.counts + i, kLnRefused);
+    }
     __syncwarp();
   }
   tc_fence_before();
