@@ -56,17 +56,24 @@ struct LnEpilogue {
 };
 
 // ---------------------------------------------------------------- epilogue
+// Sigmoid by the exponential of -|z|, which never overflows: 1 / (1 + exp(-z)) is 0 below z = -88.72, where SiLU, z times
+// it, is still 2e-37. The divisor is in [1, 2].
+__device__ __forceinline__ float ln_sigmoid(float z) {
+  const float e = expf(-fabsf(z)), r = recip_rn(__fadd_rn(1.0f, e));
+  return z < 0.0f ? __fmul_rn(e, r) : r;
+}
+
 // NaN stays NaN in each.
 __device__ __forceinline__ float ln_act(float z, int act) {
   switch (act) {
     case FME_ACT_RELU:
       return z < 0.0f ? 0.0f : z;
     case FME_ACT_SILU:
-      return silu_rn(z);
+      return __fmul_rn(z, ln_sigmoid(z));
     case FME_ACT_GELU:  // z P(N(0, 1) < z); erfc keeps the tail's relative precision, which 1 + erf loses
       return __fmul_rn(__fmul_rn(0.5f, z), erfcf(__fmul_rn(z, -0.70710678f)));
     case FME_ACT_SIGMOID:
-      return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-z)));
+      return ln_sigmoid(z);
     default:
       return z;
   }
@@ -114,10 +121,13 @@ __device__ __forceinline__ uint32_t ln_bf16x2(float lo, float hi) {
   return r;
 }
 
-// For outputs of 8 bits' precision: the hardware's approximate reciprocal (a few 2^-23).
-__device__ __forceinline__ float ln_recip_approx(float d) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+// 256 sigmoid(z) for outputs of 8 bits' precision: the hardware's approximate exponential and reciprocal, of the divisor by
+// 256, so that neither overflows nor is flushed to zero before SiLU is below the normal numbers (z = -92.9). Argument,
+// exponential and reciprocal together: 4 + 1.2 |z| units of 2^-23.
+__device__ __forceinline__ float ln_sigmoid256(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(z, -1.44269504f, -8.0f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(0x1p-8f, e)));
   return r;
 }
 
@@ -140,10 +150,10 @@ __device__ __forceinline__ void ln_finish16(const LnEpilogue& e, const float* bi
   if (act == FME_ACT_NONE) return;
   if (act == FME_ACT_SILU && !e.out_f32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = __fmul_rn(z[i], ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i]))));
+    for (int i = 0; i < 16; ++i) z[i] = __fmul_rn(__fmul_rn(z[i], 0x1p-8f), ln_sigmoid256(z[i]));
   } else if (act == FME_ACT_SIGMOID && !e.out_f32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = ln_recip_approx(__fadd_rn(1.0f, __expf(-z[i])));
+    for (int i = 0; i < 16; ++i) z[i] = __fmul_rn(ln_sigmoid256(z[i]), 0x1p-8f);
   } else if (act == FME_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = ln_act(z[i], FME_ACT_RELU);

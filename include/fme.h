@@ -584,6 +584,15 @@ int fme_block_norm(const void* x, long long ldx, const float* route_weights, int
  * layer's dense projections (no counterpart in the pages). Sums, activation
  * and residual addition are FP32, rounded once to the output's type.
  *
+ * How sums are taken: the tensor cores add FP32 by truncation. For up to 8
+ * tokens (16 with up to 2^22 weights) and for FP32 outputs their sums of at most
+ * 1024 products are added with rounding. For BF16 outputs of more tokens they
+ * add all of K (each 16 products a truncation of at most 2^-23 of the sum so
+ * far: 8e-6 of the result at K = 7168, in proportion to K beyond), and SiLU and
+ * sigmoid take the hardware's approximate exponential and reciprocal (4 + 1.2
+ * |z| units of 2^-23). Both are far below the output's rounding, but the last
+ * bit of a BF16 row may hang on how many rows stand beside it.
+ *
  * Arguments: x [M, K] BF16 with row stride ldx, w [N, K] BF16 with row stride
  *   ldw, bias [N] FP32 or NULL, activation an fme_activation, residual [M, N]
  *   of the output's type with row stride ldr, or NULL, out [M, N] of out_dtype
