@@ -788,7 +788,7 @@ def moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, sc
     BF16 unweighted route rows, ids, weights), which moe_finalize or block_norm combine."""
     _need_prompt(xq, sx, logits, bias, w13, w2)
     ws = workspaces or (None, None, None)
-    if (score, groups, renormalise) == ("sigmoid", 1, True) and bias is not None:
+    if (score, groups, renormalise) == ("sigmoid", 1, True) and bias is not None and group_top is None:
         if top_groups not in (None, 1):
             raise ValueError(f"top_groups={top_groups} of one group")
         ids, weights, offsets, rows, tokens = moe_route(logits, bias, top_k, scale, workspace=ws[0])

@@ -54,3 +54,25 @@ def test_workspaces_of_a_block_serve_every_fewer_tokens(fme):
             assert fme.moe_route_workspace(t, E, k) <= ws[0].nbytes and fme.linear_bf16_workspace(t, E, H) <= ws[3].nbytes
     # A product of more tokens than any that cuts K needs no more.
     assert fme.moe_prompt_workspaces(1 << 20, 256, 128, 8, 2, "cpu", router=True)[3].nbytes <= 1 << 25
+
+
+def test_rows_pass_every_option_of_the_routing_on(fme, monkeypatch):
+    """moe_route knows no groups: whatever is asked of them goes to the call that checks it."""
+    args, _ = _operands()
+    plain, scored = [], []
+    monkeypatch.setattr(fme, "moe_route", _stop(plain))
+    monkeypatch.setattr(fme, "moe_route_groups", _stop(scored))
+
+    def call(**kw):
+        for fn in (fme.moe_prompt_rows_fp8, fme.moe_prompt_fp8):
+            with pytest.raises(_Reached):
+                fn(**{**args, **kw})
+
+    call(), call(top_groups=1)
+    assert len(plain) == 4 and not scored
+    call(group_top=2)
+    assert len(plain) == 4 and len(scored) == 2 and all(2 in a for a, _ in scored)
+    call(group_top=7), call(group_top=1, top_groups=1), call(renormalise=False), call(score="softmax"), call(bias=None)
+    assert len(plain) == 4 and len(scored) == 12
+    with pytest.raises(ValueError, match="top_groups"):
+        fme.moe_prompt_fp8(**args, top_groups=2)
