@@ -787,6 +787,12 @@ def moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, sc
     tokens' rows and moe_grouped_gemm_fp8 back to route order. Arguments as moe_prompt_fp8. Returns (out [T * top_k, H]
     BF16 unweighted route rows, ids, weights), which moe_finalize or block_norm combine."""
     _need_prompt(xq, sx, logits, bias, w13, w2)
+    return _prompt_rows(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, workspaces, score, groups,
+                        top_groups, group_top, renormalise)
+
+
+def _prompt_rows(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, workspaces, score, groups, top_groups,
+                 group_top, renormalise):
     ws = workspaces or (None, None, None)
     if (score, groups, renormalise) == ("sigmoid", 1, True) and bias is not None and group_top is None:
         if top_groups not in (None, 1):
@@ -812,8 +818,8 @@ def moe_prompt_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, 
     ones. Without workspaces (moe_prompt_workspaces) the binding's kept ones serve, whose device errors
     kept_workspace_error reads; a graph that is to report its errors needs workspaces of the caller's."""
     _need_prompt(xq, sx, logits, bias, w13, w2, shared_out)
-    out, ids, weights = moe_prompt_rows_fp8(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0,
-                                            workspaces, score, groups, top_groups, group_top, renormalise)
+    out, ids, weights = _prompt_rows(xq, sx, logits, bias, w13, s13, w2, s2, top_k, limit, scale, ue8m0, workspaces, score,
+                                     groups, top_groups, group_top, renormalise)
     if xq.shape[0] == 0:
         return out, ids, weights
     return moe_finalize(out, weights, shared_out), ids, weights

@@ -76,3 +76,16 @@ def test_rows_pass_every_option_of_the_routing_on(fme, monkeypatch):
     assert len(plain) == 4 and len(scored) == 12
     with pytest.raises(ValueError, match="top_groups"):
         fme.moe_prompt_fp8(**args, top_groups=2)
+
+
+def test_prompt_operands_are_checked_once(fme, monkeypatch):
+    args, _ = _operands()
+    checks, seen = [], []
+    need = fme._need_prompt
+    monkeypatch.setattr(fme, "_need_prompt", lambda *a, **kw: checks.append(need(*a, **kw)))
+    monkeypatch.setattr(fme, "moe_route", _stop(seen))
+    for fn in (fme.moe_prompt_fp8, fme.moe_prompt_rows_fp8):
+        checks.clear()
+        with pytest.raises(_Reached):
+            fn(**args)
+        assert len(checks) == 1
