@@ -600,8 +600,9 @@ __global__ void __launch_bounds__(32 * rt_warps<J>()) route_kernel(const RtArgs 
         for (int e = threadIdx.x; e <= a.E; e += kRtThreads) a.offsets[e] = 0;
       return;
     }
-    // Eight experts a load; the CTAs' rows are dealt to as many threads as there are to a column.
-    const int words = a.pitch / 8, lanes = kRtThreads / words, col = threadIdx.x % words, first = threadIdx.x / words;
+    // Eight experts a load; the CTAs' rows are dealt to as many threads as there are to a column, those that get none have
+    // nothing to add (of few experts most: 8 experts, 1533 tokens 10.4 us with their zeros, 7.0 without).
+    const int words = a.pitch / 8, lanes = min(kRtThreads / words, G), col = threadIdx.x % words, first = threadIdx.x / words;
     if (first < lanes) {
       constexpr int kRows = J <= 8 ? 5 : 12;  // on their way at once
       uint32_t pair[4] = {0u, 0u, 0u, 0u}, pair_prev[4] = {0u, 0u, 0u, 0u};
