@@ -256,6 +256,7 @@ __device__ __forceinline__ void bn_token(const BnArgs& a, int t, int first, int 
         static_cast<uint8_t*>(a.scales)[static_cast<size_t>(t) * (a.H / 32) + ch / 4] = static_cast<uint8_t>(e + 127);
     } else {
       float s = quotient_rn(fmaxf(amax, 1e-10f), 448.0f, 1.0f / 448.0f);
+      if (amax == INFINITY) s = INFINITY;  // (whose residual is NaN)
       if (a.ue8m0) s = ue8m0_ceil(s);
       inv = bn_recip(s);
       if ((ch & 15) == 0) static_cast<float*>(a.scales)[static_cast<size_t>(t) * (a.H / 128) + ch / 16] = s;
