@@ -3,7 +3,7 @@
 // Three kernels.
 //
 // linear_one_kernel, one token: a warp (or 2, 4, 8 that share its K range) multiplies kLnRows weight rows, 16 bytes of each
-// a lane and load. Bound by latency where the weights are few (256 x 7168: 2.7 us) and by their stream where they are many
+// a lane and load. Bound by latency where the weights are few (256 x 7168: 2.7 us, from HBM 3.8) and by their stream where they are many
 // (4096 x 7168: 13 us, 4.4 TB/s).
 //
 // linear_few_kernel, up to 16 tokens (ln_few): warps hold 16 tokens x 8 weight rows in mma.sync fragments, loaded straight
@@ -15,14 +15,16 @@
 // issues tcgen05.mma kind::f16, eight read the accumulators (two buffers in tensor memory, so that a tile's epilogue runs
 // beside the next tile's products). Where the tiles are fewer than SMs, K is cut, too: a unit's epilogue warps then store their
 // FP32 sums to the workspace, and of a tile's units the last to have a warp's part there adds them in K order, whichever it is,
-// so the result does not hang on the order of arrival, and no unit waits for another. (A warp's parts in 16-byte pieces, counted
-// by one release and acquire a warp: 128 x 256 x 7168 FP32 9.2 us; value by value behind barriers and fences of the CTA 11.8.)
+// so the result does not hang on the order of arrival, and no unit waits for another. Counts that no call left are found and the
+// workspace refused until it is cleared. (A warp's parts in 16-byte pieces, counted by one release and acquire a warp: 128 x 256
+// x 7168 FP32 9.2 us; value by value behind barriers and fences of the CTA 11.8.)
 // * A stage holds as many K blocks of 64 values as fit 64 KB: a TMA instruction costs its warp about 100 ns whatever it
 //   brings (16 tokens x 7168 x 2048: 12.3 us with one block a stage and one loading warp, 7.8 with eight and two).
 // * FP32 outputs: the tensor core's accumulation truncates, so a chain of 448 instructions (K = 7168) is 8e-6 of the result
 //   off. Accumulations of about kLnChunk blocks are added with rounding instead: 5e-7. They stand side by side in tensor memory
 //   where a unit's fit (128 x 256 x 7168 9.2 -> 7.8 us), else they are added in registers as they end (CHUNKED: 16384 x 256 x
 //   7168 57.5 us, the chain 53.8). BF16 outputs, whose rounding is 250 times that, take the chain.
+// (Times of 64 x 7168 x 2048 below are with its weights in L2, as repeated calls find them; from HBM it takes 9.1 us.)
 // What bounds it: large products shared memory's 128 bytes a clock. A K block of a 128 x 256 tile is written there (48 KB)
 // and read by the MMAs (48 KB), 750 clocks against 512 of MMA; measured 744 (16384 x 4096 x 7168: 575 us, 1670 TFLOP/s, in a
 // burst; 615 to 640 at the power limit. The tiles' order counts: 771 us with the row tiles of one weight tile one after
@@ -420,7 +422,7 @@ constexpr int kLnEpiWarps = 8;
 constexpr int kLnLaunchRegs = 168, kLnEpiRegs = 216, kLnOtherRegs = 72;
 static_assert(2 * kLnEpiRegs + kLnOtherRegs == 3 * kLnLaunchRegs, "register split");
 constexpr int kLnMaxUnits = 160;           // units of a call that cuts K (one a CTA)
-constexpr int kLnKBlock = 64;              // values a stage: 128 bytes a row
+constexpr int kLnKBlock = 64;              // values of a K block: 128 bytes a row; a stage holds up to eight blocks
 constexpr int kLnMaxStages = 12;
 constexpr int kLnRingBytes = 196608;       // 4 stages of 128 + 256 rows
 constexpr int kLnStageBytes = 65536;
@@ -867,13 +869,14 @@ static bool ln_map(CUtensorMap* map, const void* base, int rows, int cols, long 
 
 // Whether a product goes to the kernels of few tokens. Measured with the weights out of L2, they against tiles (us): 8 tokens of
 // 256 x 7168 4.6 / 6.3, of 7168 x 2048 8.4 / 8.9, of 4096 x 7168 13.1 / 14.6; 16 tokens of 256 x 7168 5.8 / 6.4, of 1024 x
-// 4096 4.9 / 5.8, of 7168 x 1024 9.3 / 6.6, of 4096 x 7168 23 / 14.5.
+// 4096 4.9 / 5.8, of 7168 x 1024 9.3 / 6.6, of 4096 x 7168 23 / 14.5. (Weights above 4096 x 7168 were not measured.)
 static bool ln_few(int M, int N, int K) {
   return M <= 8 || (M <= kLnFewMax && static_cast<long long>(N) * K <= (1 << 22));
 }
 
 // How a product in tiles is cut: by what the ways cost, in clocks, to within 1 % on average of the best way of 42 shapes that
-// were swept with their operands out of L2 (tokens 17 to 16384, 8 to 7168 outputs, K 64 to 7168). A K block costs shared
+// were swept with their operands out of L2 (tokens 17 to 16384, 8 to 7168 outputs, K 64 to 7168); the worst are 17 x 256 x 7168
+// FP32, 7.5 % off (16 columns in 9 cuts for 8), and 200 x 256 x 7168 FP32, 6.9 % (16 columns in 4 for 32 in 8). A K block costs shared
 // memory's time at 128 bytes a clock: what is written, the box's token rows and the weight rows, and what an MMA reads, 128 (or
 // 64) token rows and the weight rows again, each of them 128 bytes; all blocks together at least HBM's, 3500 bytes a clock.
 // Cutting K costs 2500 clocks and the partial sums' way at 20 bytes a clock.
@@ -1000,7 +1003,8 @@ static int linear_few(const Linear& l, int sms, cudaStream_t st) {
   a.ldw = l.ldw;
   a.K = l.K;
   a.e = ln_epilogue(l);
-  // More warps share a row's K range while there are fewer than 16 warps an SM and each keeps two loads a lane.
+  // More warps share a row's K range while there are fewer than 16 warps an SM and each keeps one 16-byte load a lane and row
+  // (one token) or one step of 32 values (a few).
   a.share = 1;
   if (l.M == 1) {
     const int pairs = (l.N + kLnRows - 1) / kLnRows;
