@@ -430,7 +430,8 @@ __device__ __forceinline__ void rt_pick_scored(const RtArgs& a, Bias load_bias, 
   uint32_t ky[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(a.bias != nullptr ? p[j] : l[j])) : 0u;
+    // (Adding 0 makes -0 the same key as 0; score + bias is never -0.)
+    ky[j] = J * lane + j < a.E ? max(1u, ordered_key(a.bias != nullptr ? p[j] : __fadd_rn(l[j], 0.0f))) : 0u;
   }
   if (a.top_groups < a.groups) {
     uint32_t open;
