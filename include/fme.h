@@ -433,6 +433,7 @@ int fme_add_rmsnorm_mxfp8(const void* x, long long ldx, const void* residual, lo
  *   route at each place) and tokens [T * top_k] int32 (its token, route /
  *   top_k). 0 <= T <= 2^20 (0: offsets are zeroed), E in [1, 1024], top_k in
  *   [1, min(E, 32)]. NaN logits give picks that are distinct and in range.
+ *   Outputs must not overlap an input or one another.
  *   Every pointer 16-byte aligned. The workspace (see
  *   fme_moe_route_workspace) must be zeroed before its first use; a
  *   workspace sized for T serves every smaller T. A call whose CTAs could not

@@ -60,3 +60,33 @@ def test_a_prompt_of_one_workspace(fme):
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(layer(one, (one, one, one)), want))
     assert one.error() == 0
+
+
+def test_graphs_and_streams_of_cut_products_share_nothing(fme):
+    """Two graphs of routing and a cut product, replayed side by side on two streams beside calls on a third."""
+    T, E, k, (M, N, K) = 1350, 384, 6, (20, 16, 3584)
+    logits, bias = torch.randn(T, E, device=DEV), 0.1 * torch.randn(E, device=DEV)
+    x, w = torch.randn(M, K, device=DEV).to(BF), torch.randn(N, K, device=DEV).to(BF)
+
+    def step():
+        return [*fme.moe_route(logits, bias, k), fme.linear_bf16(x, w), fme.linear_bf16(x, w, out_dtype=torch.float32)]
+
+    want = step()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(step())
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = step()
+    torch.cuda.synchronize()
+    for got in (*outs, eager):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert fme.kept_workspace_error() == 0
